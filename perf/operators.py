@@ -35,19 +35,20 @@ def listed():
          "block_rows": 128, "plain": True, "turned": True},
         # One token through a square projection: the weight's bytes are everything.
         {"name": "product_token", "op": "product", "M": 1, "N": 4096, "K": 4096, "out": "bf16",
-         "bias": False, "act": 0, "b_rows": 128, "pad": 0},
+         "bias": False, "act": 0, "b_rows": 128, "pad": 0, "fast": True},
         # A small serving batch through the up projection, with its bias and activation.
         {"name": "product_batch", "op": "product", "M": 64, "N": 14336, "K": 4096, "out": "bf16",
-         "bias": True, "act": 1, "b_rows": 128, "pad": 0},
+         "bias": True, "act": 1, "b_rows": 128, "pad": 0, "fast": True},
         # The framework's feed-forward workload: 4096 tokens, bias and GELU.
         {"name": "product_ffn", "op": "product", "M": 4096, "N": 14336, "K": 4096, "out": "f16",
-         "bias": True, "act": 1, "b_rows": 128, "pad": 0},
-        # A weight gradient: both operands scaled by row blocks along the tokens, float32 result.
+         "bias": True, "act": 1, "b_rows": 128, "pad": 0, "fast": True},
+        # A weight gradient: both operands scaled by row blocks along the tokens, float32 result and
+        # float32 sums throughout (the 16-bit results above take the 8-bit instructions' own sums).
         {"name": "product_wgrad", "op": "product", "M": 4096, "N": 4096, "K": 8192, "out": "f32",
-         "bias": False, "act": 0, "b_rows": 1, "pad": 0},
+         "bias": False, "act": 0, "b_rows": 1, "pad": 0, "fast": False},
         # The framework's ragged shape: no size a multiple of a tile, rows padded to 16 bytes.
         {"name": "product_ragged", "op": "product", "M": 1000, "N": 3000, "K": 777, "out": "bf16",
-         "bias": True, "act": 0, "b_rows": 128, "pad": 7},
+         "bias": True, "act": 0, "b_rows": 128, "pad": 7, "fast": True},
         # One token of a small model's layer: launches and latency.
         {"name": "moe_small", "op": "moe", "T": 1, "D": 1024, "I": 512, "E": 8, "k": 2,
          "type": "bf16", "weights": "bf16", "act": 2, "gated": True, "norm": True, "pad": 0},
@@ -86,7 +87,8 @@ def draw(rng):
             case = {"op": op, "M": _size(rng, 1, 8192, 16), "N": _size(rng, 64, 16384, 64),
                     "K": _size(rng, 64, 16384, 128), "out": rng.choice(["bf16", "f16", "f32"]),
                     "bias": rng.random() < 0.5, "act": rng.choice([0, 0, 1, 2]),
-                    "b_rows": rng.choice([128, 128, 1]), "pad": 0}
+                    "b_rows": rng.choice([128, 128, 1]), "pad": 0, "fast": False}
+            case["fast"] = case["out"] != "f32" and rng.random() < 0.75
             case["pad"] = -case["K"] % 16 if rng.random() < 0.75 else 0
             if case["M"] * case["N"] * case["K"] <= 4096 * 14336 * 4096:
                 return case
@@ -219,7 +221,7 @@ def _run_own(s):
     if s["op"] == "product":
         lib.fp8_gemm_bias_act(s["M"], s["N"], s["K"], 1.0, s["A"], s["ld"], s["SA"], s["SA"].shape[1],
                               s["B"], s["ld"], s["SB"], s["SB"].shape[1], s["b_rows"], s["bias_v"],
-                              s["act"], types[s["out"]], s["C"], s["N"])
+                              s["act"], types[s["out"]], s["C"], s["N"], fast_sums=s["fast"])
         return [s["C"]]
     shape = lib.MoeShape(tokens=s["T"], d_model=s["D"], d_ff=s["I"], experts=s["E"], top_k=s["k"],
                          type=types[s["type"]], weight_type=types[s["weights"]], act=s["act"],
