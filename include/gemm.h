@@ -38,6 +38,7 @@
 #ifndef LINEAR_ALGEBRA_SGEMM_AMD_GEMM_H
 #define LINEAR_ALGEBRA_SGEMM_AMD_GEMM_H
 
+#include <stddef.h>
 #include <stdint.h>
 #include <hip/hip_runtime_api.h>
 
@@ -56,8 +57,19 @@ typedef enum {
 
 typedef enum {
   GEMM_ACT_NONE = 0,      /* identity */
-  GEMM_ACT_GELU_TANH = 1  /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+  GEMM_ACT_GELU_TANH = 1, /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+  GEMM_ACT_SILU = 2       /* x / (1 + exp(-x)): the 8-bit product and moe_ffn only */
 } gemm_act_t;
+
+/* Element types of the 8-bit operators and moe_ffn.  E4M3 is the 8-bit format
+ * of 4 exponent and 3 mantissa bits with a NaN (bit patterns 0x7f, 0xff), no
+ * infinity and the largest value 448. */
+typedef enum {
+  GEMM_TYPE_F32 = 0,
+  GEMM_TYPE_F16 = 1,
+  GEMM_TYPE_BF16 = 2,
+  GEMM_TYPE_E4M3 = 3
+} gemm_type_t;
 
 /*
  * Initialise the library for the current HIP device.  Checks that the device
@@ -131,6 +143,88 @@ int bgemm_bias_act(int M, int N, int K, float alpha,
                    const uint16_t* A, int lda, const uint16_t* B, int ldb,
                    const float* bias, int act,
                    uint16_t* C, int ldc, hipStream_t stream);
+
+/*
+ * Block quantisation to e4m3.  With s = max(max|x| / 448, 2^-126) over a block
+ * of `block_rows` (1 or 128) rows and 128 columns of X (rows x cols, `type`
+ * F32, F16 or BF16; the last blocks of a row or column may be shorter),
+ *   Q[i][j] = x[i][j] / s, rounded to e4m3 to nearest even,
+ *   S[j / 128][i] = s  (block_rows 1)  or  S[j / 128][i / 128] = s  (128),
+ * Q rows x cols with leading dimension ldq >= cols, S with lds >= rows, or >=
+ * ceil(rows / 128).  QT, ST: the same of the transpose of X: QT cols x rows
+ * (ldqt >= rows), blocks of 128 rows of X by one column (ST[i / 128][j]) or by
+ * 128 (ST[i / 128][j / 128]), ldst >= cols or ceil(cols / 128).  Q with S, or
+ * QT with ST, may be null (their leading dimensions are then ignored), not
+ * both pairs.  A block that holds a NaN has a NaN scale and NaN values; one that holds an
+ * infinity an infinite scale, NaN for its infinities and 0 for the rest.
+ * rows == 0 or cols == 0: nothing is done.
+ */
+int fp8_quantize(int rows, int cols, int type, const void* X, int ldx, int block_rows,
+                 uint8_t* Q, int ldq, float* S, int lds,
+                 uint8_t* QT, int ldqt, float* ST, int ldst, hipStream_t stream);
+
+/*
+ * The block-scaled e4m3 product with fused bias and activation,
+ *   C[m][n] = act(alpha sum_k SA[k / 128][m] A[m][k] SB[k / 128][n / b_rows] B[n][k] + bias[n]),
+ * A M x K (lda >= K) and B N x K (ldb >= K; the transposed operand, as
+ * fp8_quantize's outputs are laid out), ldsa >= M, b_rows 1 or 128 with ldsb >=
+ * N or ceil(N / 128), an FP32 bias of length N (NULL = none), `act` of
+ * gemm_act_t, C of `type` F32, F16 or BF16, rounded once to nearest even.
+ * Bytes of A and B past column K are not used.  alpha == 0 or K == 0: A, B and
+ * the scales are not read.
+ * fast_sums 0: each block's sum is formed in fp32 from exact products.
+ * fast_sums 1: by the 8-bit matrix instructions, at twice the rate; their adder
+ * drops what lies below about 2^-13 of the largest product it adds at once,
+ * which was measured to cost up to 1e-5 (data of one magnitude) to 2e-4
+ * (magnitudes over several powers of ten) of sum_k |a||b| of a block: meant for
+ * 16-bit results.  The sums over blocks are fp32 either way.
+ */
+int fp8_gemm_bias_act(int M, int N, int K, float alpha,
+                      const uint8_t* A, int lda, const float* SA, int ldsa,
+                      const uint8_t* B, int ldb, const float* SB, int ldsb, int b_rows,
+                      const float* bias, int act, int type, void* C, int ldc,
+                      int fast_sums, hipStream_t stream);
+
+/* A mixture-of-experts feed-forward layer (moe_ffn). */
+typedef struct {
+  int tokens;       /* T, 0 .. 64 */
+  int d_model;      /* D, 1 .. 2^20 */
+  int d_ff;         /* I, 1 .. 2^20 */
+  int experts;      /* E, 1 .. 1024 */
+  int top_k;        /* k, 1 .. min(E, 32) */
+  int type;         /* of X, R and Y: F16 or BF16 */
+  int weight_type;  /* of W1 and W2: `type` or E4M3 */
+  int act;          /* gemm_act_t */
+  int gated;        /* 1: W1 has 2 I rows, and act(first I) multiplies the second I */
+  int norm_topk;    /* 1: a token's k weights are divided by their sum */
+} moe_shape_t;
+
+/* Bytes of device memory a moe_ffn call of this shape needs as `workspace`. */
+int moe_ffn_workspace(const moe_shape_t* shape, size_t* bytes);
+
+/*
+ * The layer, for the few tokens of a decoding step:
+ *   l = X R^T (T x E),  ids[t] = the k largest of l[t], largest first, equal
+ *   ones by lower number,  w[t] = softmax(l[t]) at ids[t] (divided by their sum
+ *   with norm_topk),  Y[t] = sum_s w[t][s] W2[e] h(W1[e] X[t]),  e = ids[t][s],
+ *   h(u) = act(u), or with `gated` act(u[0 .. I)) u[I .. 2 I).
+ * X T x D (ldx), R E x D (ldr), W1 E matrices of (gated ? 2 I : I) x D (ld1)
+ * one behind the other, W2 E matrices of D x I (ld2), ids (int32) and w (FP32)
+ * T x k dense, Y T x D (ldy).  With E4M3 weights S1 and S2 hold a scale for every 128 x
+ * 128 block of each matrix, expert by expert, column block by column block:
+ * S1[e][d / 128][row / 128], S2[e][i / 128][d / 128], dense; else they are
+ * ignored.  Columns past D or I of a row are not used.
+ * The logits and the choice are computed in 64 bits, products with fp32 sums;
+ * h is kept as two numbers of `type`, so in F16 its range is +-65504 (larger
+ * finite values are clamped to that).
+ * `workspace` (256-byte aligned, at least moe_ffn_workspace bytes) belongs to
+ * the call until its work on `stream` is done; its contents need no
+ * preparation.  tokens == 0: nothing is done.
+ */
+int moe_ffn(const moe_shape_t* shape, const uint16_t* X, int ldx, const uint16_t* R, int ldr,
+            const void* W1, int ld1, const float* S1, const void* W2, int ld2, const float* S2,
+            int* ids, float* w, uint16_t* Y, int ldy, void* workspace, size_t workspace_bytes,
+            hipStream_t stream);
 
 /* Static text for a status code; for GEMM_STATUS_HIP_ERROR it also names the
  * last HIP error seen by the library on this host thread. */

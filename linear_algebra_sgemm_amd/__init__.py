@@ -15,11 +15,13 @@ import ctypes
 import os
 
 __all__ = ["GemmError", "gemm_create", "gemm_destroy", "sgemm", "sgemm_noalloc", "hgemm_bias_act",
-           "bgemm_bias_act",
+           "bgemm_bias_act", "fp8_quantize", "fp8_gemm_bias_act", "MoeShape", "moe_ffn_workspace",
+           "moe_ffn",
            "gemm_status_string", "gemm_debug_force_tile", "gemm_debug_force_splits",
            "gemm_debug_pick_config", "gemm_debug_use_tuned_table", "gemm_debug_force_swizzle",
            "gemm_debug_tile_map", "library_path",
-           "load_library", "EXPORTED_SYMBOLS", "ACT_NONE", "ACT_GELU_TANH"]
+           "load_library", "EXPORTED_SYMBOLS", "ACT_NONE", "ACT_GELU_TANH", "ACT_SILU",
+           "TYPE_F32", "TYPE_F16", "TYPE_BF16", "TYPE_E4M3"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libgemm.so")
@@ -33,15 +35,28 @@ STATUS_INTERNAL = 5
 
 ACT_NONE = 0
 ACT_GELU_TANH = 1
+ACT_SILU = 2   # fp8_gemm_bias_act and moe_ffn only
+
+TYPE_F32 = 0
+TYPE_F16 = 1
+TYPE_BF16 = 2
+TYPE_E4M3 = 3
 
 # Every symbol declared in include/gemm.h and include/gemm_debug.h.
 EXPORTED_SYMBOLS = ("gemm_create", "gemm_destroy", "sgemm", "sgemm_noalloc", "hgemm_bias_act",
-                    "bgemm_bias_act",
+                    "bgemm_bias_act", "fp8_quantize", "fp8_gemm_bias_act", "moe_ffn_workspace",
+                    "moe_ffn",
                     "gemm_status_string", "gemm_debug_force_tile", "gemm_debug_force_splits",
                     "gemm_debug_pick_config", "gemm_debug_use_tuned_table",
                     "gemm_debug_force_swizzle", "gemm_debug_tile_map")
 
 _lib = None
+
+
+class MoeShape(ctypes.Structure):
+    """moe_shape_t of include/gemm.h; every field by keyword."""
+    _fields_ = [(n, ctypes.c_int) for n in ("tokens", "d_model", "d_ff", "experts", "top_k", "type",
+                                            "weight_type", "act", "gated", "norm_topk")]
 
 
 class GemmError(RuntimeError):
@@ -76,6 +91,15 @@ def load_library():
     lib.hgemm_bias_act.restype = I
     lib.bgemm_bias_act.argtypes = [I, I, I, F, P, I, P, I, P, I, P, I, P]
     lib.bgemm_bias_act.restype = I
+    S, SP = ctypes.c_size_t, ctypes.POINTER(MoeShape)
+    lib.fp8_quantize.argtypes = [I, I, I, P, I, I, P, I, P, I, P, I, P, I, P]
+    lib.fp8_quantize.restype = I
+    lib.fp8_gemm_bias_act.argtypes = [I, I, I, F, P, I, P, I, P, I, P, I, I, P, I, I, P, I, I, P]
+    lib.fp8_gemm_bias_act.restype = I
+    lib.moe_ffn_workspace.argtypes = [SP, ctypes.POINTER(S)]
+    lib.moe_ffn_workspace.restype = I
+    lib.moe_ffn.argtypes = [SP, P, I, P, I, P, I, P, P, I, P, P, P, P, I, P, S, P]
+    lib.moe_ffn.restype = I
     lib.gemm_status_string.argtypes = [I]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_debug_force_tile.argtypes = [I, I]
@@ -162,6 +186,46 @@ def bgemm_bias_act(M, N, K, alpha, A, lda, B, ldb, bias, act, C, ldc, stream=Non
                                        _ptr(B), int(ldb), _ptr(bias), int(act), _ptr(C), int(ldc),
                                        _stream(stream))
     return _check(st, "bgemm_bias_act", raise_on_error)
+
+
+def fp8_quantize(rows, cols, type, X, ldx, block_rows, Q, ldq, S, lds, QT=None, ldqt=0, ST=None,
+                 ldst=0, stream=None, *, raise_on_error=True):
+    """e4m3 values and block scales of X and / or of its transpose; see include/gemm.h."""
+    st = load_library().fp8_quantize(int(rows), int(cols), int(type), _ptr(X), int(ldx),
+                                     int(block_rows), _ptr(Q), int(ldq), _ptr(S), int(lds),
+                                     _ptr(QT), int(ldqt), _ptr(ST), int(ldst), _stream(stream))
+    return _check(st, "fp8_quantize", raise_on_error)
+
+
+def fp8_gemm_bias_act(M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_rows, bias, act, type, C,
+                      ldc, stream=None, *, fast_sums=False, raise_on_error=True):
+    """C = act(alpha * A x B^T + bias), block-scaled e4m3 A and B; see include/gemm.h.
+
+    fast_sums: let the 8-bit matrix instructions form each block's sum (twice the rate, sums of
+    about 13 bits within a block of 128): for 16-bit results."""
+    st = load_library().fp8_gemm_bias_act(int(M), int(N), int(K), float(alpha), _ptr(A), int(lda),
+                                          _ptr(SA), int(ldsa), _ptr(B), int(ldb), _ptr(SB),
+                                          int(ldsb), int(b_rows), _ptr(bias), int(act), int(type),
+                                          _ptr(C), int(ldc), int(fast_sums), _stream(stream))
+    return _check(st, "fp8_gemm_bias_act", raise_on_error)
+
+
+def moe_ffn_workspace(shape: MoeShape) -> int:
+    """Bytes of device memory a moe_ffn call of this shape needs as its workspace."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_ffn_workspace(ctypes.byref(shape), ctypes.byref(n)),
+           "moe_ffn_workspace", True)
+    return n.value
+
+
+def moe_ffn(shape, X, ldx, R, ldr, W1, ld1, S1, W2, ld2, S2, ids, w, Y, ldy, workspace,
+            workspace_bytes, stream=None, *, raise_on_error=True):
+    """A mixture-of-experts feed-forward layer for up to 64 tokens; see include/gemm.h."""
+    st = load_library().moe_ffn(ctypes.byref(shape), _ptr(X), int(ldx), _ptr(R), int(ldr), _ptr(W1),
+                                int(ld1), _ptr(S1), _ptr(W2), int(ld2), _ptr(S2), _ptr(ids),
+                                _ptr(w), _ptr(Y), int(ldy), _ptr(workspace), int(workspace_bytes),
+                                _stream(stream))
+    return _check(st, "moe_ffn", raise_on_error)
 
 
 def gemm_status_string(status: int) -> str:

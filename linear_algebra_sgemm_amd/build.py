@@ -21,7 +21,8 @@ LIB_NAME = "libgemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["gemm_capi.cpp", "gemm_config.cpp", "sgemm_kernels.hip", "hgemm_kernels.hip",
-           "pack_kernels.hip"]
+           "pack_kernels.hip", "lm_capi.cpp", "quantize_kernels.hip", "fp8_kernels.hip",
+           "moe_kernels.hip"]
 ARCH = "gfx950"
 
 DEVICE_FLAGS = [
@@ -41,7 +42,7 @@ def hipcc() -> str:
     return path
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def build(verbose: bool = False, jobs: int = 8) -> str:
     """Compile every source to an object (in parallel) and link libgemm.so; return its path."""
     cc = hipcc()
     tmpdir = tempfile.mkdtemp(prefix="lasg_build_")

@@ -1,0 +1,219 @@
+// The block-scaled e4m3 product with bias and activation fused into the single
+// write-back:
+//     C[m][n] = act(alpha sum_kb SA[kb][m] SB[kb][n] P_kb[m][n] + bias[n]),
+//     P_kb[m][n] = sum over the 128 columns k of block kb of A[m][k] B[n][k],
+// A (M x K) and B (N x K) in e4m3, both contiguous along K; SA holds one scale
+// per row and block, SB one per row, or per 128 rows, and block (both
+// block-major: the scales of one block of columns lie together).
+//
+// Each block's sum P_kb is formed by MFMAs from zero and added to fp32 totals
+// with the product of its two scales, since the scales are arbitrary fp32
+// numbers and the matrix unit's own block scales are powers of two.
+//
+// Two ways to form P_kb:
+//  * fast sums: the 8-bit MFMAs (v_mfma_f32_*_f8f6f4).  Their internal adder
+//    aligns the products of one instruction to the largest and drops what falls
+//    below about 2^-13 of it (measured over 128 columns: up to 9e-6 of
+//    sum |a||b| for normal data, 1.7e-4 where magnitudes spread over several
+//    powers of ten), so a caller asks for them.  4643 TFLOP/s in a loop of nothing else.
+//  * else the operands are widened to bfloat16, which is exact, and multiplied
+//    by the 16-bit MFMAs, whose sums are fp32 (2e-7 on the same data): half the rate.
+//
+// Operand k order: an MFMA pairs the same lane and byte of both operands, so
+// any assignment of k to lanes serves if both use it.
+#include "lm_common.h"
+#include "lm_launch.h"
+
+namespace lasg {
+
+namespace {
+
+// One 16-row fragment of 128 k: lane l holds row l % 16, the 16-byte chunks
+// l / 16 and l / 16 + 4 of its eight.
+struct Frag {
+  u32x4 c[2];
+};
+
+__device__ __forceinline__ void load_frag(Frag& f, const uint8_t* row, int lane, int valid) {
+  const int g = 16 * (lane / 16);
+  if (valid >= kBlockK) {   // (uniform over the wave)
+    f.c[0] = load16(row + g);
+    f.c[1] = load16(row + g + 64);
+  } else {
+    f.c[0] = load16_upto(row + g, valid - g);
+    f.c[1] = load16_upto(row + g + 64, valid - g - 64);
+  }
+}
+
+template <bool FAST>
+__device__ __forceinline__ f32x4 block_product(const Frag& x, const Frag& y) {
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (FAST) {
+    i32x8 a, b;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = (int)x.c[e / 4][e % 4];
+      b[e] = (int)y.c[e / 4][e % 4];
+    }
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      acc = LmBF16::mfma(widen_bf16(x.c[h / 2][2 * (h % 2)], x.c[h / 2][2 * (h % 2) + 1]),
+                         widen_bf16(y.c[h / 2][2 * (h % 2)], y.c[h / 2][2 * (h % 2) + 1]), acc);
+    return acc;
+  }
+}
+
+// Four consecutive values of one row of C (columns col ..; `left` of them exist).
+__device__ __forceinline__ void store_c(const Fp8Call& p, int64_t row, int64_t col, f32x4 v) {
+  const int64_t left = p.N - col;
+  if (p.type == GEMM_TYPE_F32) {
+    float* d = static_cast<float*>(p.C) + row * p.ldc + col;
+    if (left >= 4) {
+      *reinterpret_cast<f32x4_any*>(d) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) d[e] = v[e];
+    }
+    return;
+  }
+  uint16_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    h[e] = p.type == GEMM_TYPE_F16 ? LmF16::bits(v[e]) : LmBF16::bits(v[e]);
+  uint16_t* d = static_cast<uint16_t*>(p.C) + row * p.ldc + col;
+  if (left >= 4) {
+    *reinterpret_cast<u32x2_any*>(d) = __builtin_bit_cast(u32x2, h);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) d[e] = h[e];
+  }
+}
+
+}  // namespace
+
+// 16 MF x 16 NF output tile per workgroup, its eight waves taking the blocks of
+// K in turn (wave w: blocks w, w + 8, ...) straight from memory into MFMA
+// operands, the eight totals added in LDS at the end in wave order.  Any shape,
+// stride and alignment.  Few rows: the bytes of B bound it, every one of which
+// is read once, eight consecutive 128-byte lines of a row by the eight waves.
+// ROWB: one scale per row of B (else per 128 rows: one for the tile).
+template <int MF, int NF, bool FAST, bool ROWB>
+__global__ void __launch_bounds__(512) fp8_ksplit_kernel(Fp8Call p) {
+  __shared__ __attribute__((aligned(16))) f32x4 part[8][MF * NF][kWave];
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = lane % 16, g = lane / 16;
+  const unsigned tiles_n = ((unsigned)p.N + 16 * NF - 1) / (16 * NF);
+  const unsigned tiles_m = ((unsigned)p.M + 16 * MF - 1) / (16 * MF);
+  const int kbs = (int)(((unsigned)p.K + kBlockK - 1) / kBlockK);
+  for (unsigned tm = blockIdx.y; tm < tiles_m; tm += gridDim.y)
+    for (unsigned tn = blockIdx.x; tn < tiles_n; tn += gridDim.x) {
+      const int64_t m0 = (int64_t)tm * 16 * MF, n0 = (int64_t)tn * 16 * NF;
+      // Rows past the end read the last row; what they give is never stored.
+      const uint8_t* ap[MF];
+      const uint8_t* bp[NF];
+      const float* sa[MF];
+      const float* sb[NF][ROWB ? 4 : 1];
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        const int64_t row = m0 + 16 * i + r < p.M ? m0 + 16 * i + r : p.M - 1;
+        ap[i] = p.A + row * p.lda;
+        sa[i] = p.SA + row;
+      }
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        const int64_t row = n0 + 16 * j + r < p.N ? n0 + 16 * j + r : p.N - 1;
+        bp[j] = p.B + row * p.ldb;
+        if constexpr (ROWB) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int64_t n = n0 + 16 * j + 4 * g + e;
+            sb[j][e] = p.SB + (n < p.N ? n : p.N - 1);
+          }
+        } else {
+          sb[j][0] = p.SB + n0 / kBlockK;
+        }
+      }
+      f32x4 total[MF][NF];
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) total[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int kb = wave; kb < kbs; kb += 8) {
+        const int k0 = kb * kBlockK;
+        Frag a[MF], b[NF];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) load_frag(b[j], bp[j] + k0, lane, p.K - k0);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) load_frag(a[i], ap[i] + k0, lane, p.K - k0);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          const float si = sa[i][(int64_t)kb * p.ldsa];
+#pragma unroll
+          for (int j = 0; j < NF; ++j) {
+            // (B first: the lane then holds four columns of one row of C)
+            const f32x4 v = block_product<FAST>(b[j], a[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              total[i][j][e] = __builtin_fmaf(
+                  v[e], si * sb[j][ROWB ? e : 0][(int64_t)kb * p.ldsb], total[i][j][e]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) part[wave][i * NF + j][lane] = total[i][j];
+      __syncthreads();
+      for (int f = wave; f < MF * NF; f += 8) {
+        f32x4 v = part[0][f][lane];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) v += part[w][f][lane];
+        const int64_t row = m0 + 16 * (f / NF) + r, col = n0 + 16 * (f % NF) + 4 * g;
+        if (row < p.M && col < p.N) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float b = p.bias != nullptr && col + e < p.N ? p.bias[col + e] : 0.0f;
+            v[e] = apply_act(__builtin_fmaf(p.alpha, v[e], b), p.act);
+          }
+          store_c(p, row, col, v);
+        }
+      }
+      __syncthreads();   // the next tile reuses the LDS array
+    }
+}
+
+namespace {
+
+template <int MF, int NF>
+hipError_t launch_ksplit(const Fp8Call& c, hipStream_t s) {
+  const unsigned tn = ((unsigned)c.N + 16 * NF - 1) / (16 * NF);
+  const unsigned tm = ((unsigned)c.M + 16 * MF - 1) / (16 * MF);
+  const dim3 grid(tn < (1u << 20) ? tn : (1u << 20), tm < 32768u ? tm : 32768u);
+  if (c.fast_sums) {
+    if (c.b_rows == 1)
+      fp8_ksplit_kernel<MF, NF, true, true><<<grid, 512, 0, s>>>(c);
+    else
+      fp8_ksplit_kernel<MF, NF, true, false><<<grid, 512, 0, s>>>(c);
+  } else {
+    if (c.b_rows == 1)
+      fp8_ksplit_kernel<MF, NF, false, true><<<grid, 512, 0, s>>>(c);
+    else
+      fp8_ksplit_kernel<MF, NF, false, false><<<grid, 512, 0, s>>>(c);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, hipStream_t s) {
+  (void)cus;
+  if (c.M <= 16) return launch_ksplit<1, 1>(c, s);
+  return launch_ksplit<4, 2>(c, s);
+}
+
+}  // namespace lasg

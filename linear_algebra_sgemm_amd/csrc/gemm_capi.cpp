@@ -19,6 +19,7 @@
 #include "../../include/gemm_debug.h"
 #include "gemm_common.h"
 #include "gemm_launch.h"
+#include "lm_launch.h"
 
 namespace {
 
@@ -351,6 +352,14 @@ lasg::HalfPlan decide_half(int M, int N, int K, bool a_ok, bool b_ok, int cus, s
 }
 
 }  // namespace
+
+namespace lasg {
+
+bool library_ready() { return g_ready.load() != 0; }
+int library_cus() { return g_cus.load(); }
+int library_hip_failure(hipError_t e) { return hip_failure(e); }
+
+}  // namespace lasg
 
 extern "C" {
 

@@ -1,0 +1,79 @@
+// Internal interface between the C ABI of the 8-bit operators and the
+// mixture-of-experts layer (lm_capi.cpp) and their kernels.  Arguments arrive
+// here already validated.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/gemm.h"
+
+namespace lasg {
+
+// Library state (gemm_capi.cpp): whether gemm_create has run, the compute units
+// of its device, and the status of a failed HIP call (kept for
+// gemm_status_string).
+bool library_ready();
+int library_cus();
+int library_hip_failure(hipError_t e);
+
+struct QuantizeCall {
+  int rows, cols, type;
+  const void* X;
+  int ldx;
+  int block_rows;   // 1 or 128
+  uint8_t* Q;       // null: not wanted
+  int ldq;
+  float* S;
+  int lds;
+  uint8_t* QT;      // null: not wanted
+  int ldqt;
+  float* ST;
+  int ldst;
+};
+hipError_t launch_quantize(const QuantizeCall& c, hipStream_t s);
+
+struct Fp8Call {
+  int M, N, K;      // K == 0: the product is zero and A, B are not read
+  float alpha;
+  const uint8_t* A;
+  int lda;
+  const float* SA;
+  int ldsa;
+  const uint8_t* B;
+  int ldb;
+  const float* SB;
+  int ldsb;
+  int b_rows;       // rows of B that share a scale: 1 or 128
+  const float* bias;
+  int act;
+  int type;         // of C
+  void* C;
+  int ldc;
+  bool fast_sums;
+};
+hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, hipStream_t s);
+
+struct MoeCall {
+  moe_shape_t shape;
+  const uint16_t* X;
+  int ldx;
+  const uint16_t* R;
+  int ldr;
+  const void* W1;
+  int ld1;
+  const float* S1;
+  const void* W2;
+  int ld2;
+  const float* S2;
+  int* ids;
+  float* w;
+  uint16_t* Y;
+  int ldy;
+  void* ws;
+};
+size_t moe_workspace_bytes(const moe_shape_t& s);
+hipError_t launch_moe(const MoeCall& c, int cus, hipStream_t s);
+
+}  // namespace lasg
