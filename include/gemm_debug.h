@@ -36,7 +36,10 @@ extern "C" {
  * 8 = 128 x 128 direct-to-LDS tiles at two workgroups per compute unit (tile 1
  * where the operands do not allow direct copies) and 9 = 16 x 16 tiles whose
  * eight waves split K between them (any operands; small outputs; never split
- * across workgroups).
+ * across workgroups).  op 2 = fp8_gemm_bias_act: 0 = 128 x 256 tiles (fast
+ * sums with one scale per 128 rows of B, else 1), 1 = 256 x 128 and 2 = 128 x 128
+ * tiles copied straight into LDS (else 3), 3 = 128 x 128 tiles through registers,
+ * 4 = 64 x 32 and 5 = 16 x 16 tiles whose eight waves split K between them.
  * Whether the aligned fast path or the
  * bounds-checked path runs still follows the shape and alignment.  Returns
  * GEMM_STATUS_INVALID_VALUE for an unknown op or tile.  Pure host state: no

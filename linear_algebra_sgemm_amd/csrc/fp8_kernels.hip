@@ -21,8 +21,7 @@
 //
 // Operand k order: an MFMA pairs the same lane and byte of both operands, so
 // any assignment of k to lanes serves if both use it.
-#include "lm_common.h"
-#include "lm_launch.h"
+#include "fp8_common.h"
 
 namespace lasg {
 
@@ -34,14 +33,14 @@ struct Frag {
   u32x4 c[2];
 };
 
-__device__ __forceinline__ void load_frag(Frag& f, const uint8_t* row, int lane, int valid) {
-  const int g = 16 * (lane / 16);
-  if (valid >= kBlockK) {   // (uniform over the wave)
-    f.c[0] = load16(row + g);
-    f.c[1] = load16(row + g + 64);
+__device__ __forceinline__ void load_frag(Frag& f, const uint8_t* row, int lane, int k0, int K) {
+  const int k = k0 + 16 * (lane / 16);
+  if (K - k0 >= kBlockK) {   // (uniform over the wave)
+    f.c[0] = load16(row + k);
+    f.c[1] = load16(row + k + 64);
   } else {
-    f.c[0] = load16_upto(row + g, valid - g);
-    f.c[1] = load16_upto(row + g + 64, valid - g - 64);
+    f.c[0] = load16_row(row, k, K);
+    f.c[1] = load16_row(row, k + 64, K);
   }
 }
 
@@ -62,34 +61,6 @@ __device__ __forceinline__ f32x4 block_product(const Frag& x, const Frag& y) {
       acc = LmBF16::mfma(widen_bf16(x.c[h / 2][2 * (h % 2)], x.c[h / 2][2 * (h % 2) + 1]),
                          widen_bf16(y.c[h / 2][2 * (h % 2)], y.c[h / 2][2 * (h % 2) + 1]), acc);
     return acc;
-  }
-}
-
-// Four consecutive values of one row of C (columns col ..; `left` of them exist).
-__device__ __forceinline__ void store_c(const Fp8Call& p, int64_t row, int64_t col, f32x4 v) {
-  const int64_t left = p.N - col;
-  if (p.type == GEMM_TYPE_F32) {
-    float* d = static_cast<float*>(p.C) + row * p.ldc + col;
-    if (left >= 4) {
-      *reinterpret_cast<f32x4_any*>(d) = v;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < left) d[e] = v[e];
-    }
-    return;
-  }
-  uint16_t h[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    h[e] = p.type == GEMM_TYPE_F16 ? LmF16::bits(v[e]) : LmBF16::bits(v[e]);
-  uint16_t* d = static_cast<uint16_t*>(p.C) + row * p.ldc + col;
-  if (left >= 4) {
-    *reinterpret_cast<u32x2_any*>(d) = __builtin_bit_cast(u32x2, h);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < left) d[e] = h[e];
   }
 }
 
@@ -147,9 +118,9 @@ __global__ void __launch_bounds__(512) fp8_ksplit_kernel(Fp8Call p) {
         const int k0 = kb * kBlockK;
         Frag a[MF], b[NF];
 #pragma unroll
-        for (int j = 0; j < NF; ++j) load_frag(b[j], bp[j] + k0, lane, p.K - k0);
+        for (int j = 0; j < NF; ++j) load_frag(b[j], bp[j], lane, k0, p.K);
 #pragma unroll
-        for (int i = 0; i < MF; ++i) load_frag(a[i], ap[i] + k0, lane, p.K - k0);
+        for (int i = 0; i < MF; ++i) load_frag(a[i], ap[i], lane, k0, p.K);
 #pragma unroll
         for (int i = 0; i < MF; ++i) {
           const float si = sa[i][(int64_t)kb * p.ldsa];
@@ -210,10 +181,26 @@ hipError_t launch_ksplit(const Fp8Call& c, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, hipStream_t s) {
-  (void)cus;
-  if (c.M <= 16) return launch_ksplit<1, 1>(c, s);
-  return launch_ksplit<4, 2>(c, s);
+int fp8_tile(const Fp8Call& c, int cus, int force) {
+  // 32-bit row and tile numbers in the tiled kernels.
+  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) &&
+                     ((int64_t)c.M + 127) / 128 * (((int64_t)c.N + 127) / 128) < (1 << 22);
+  int tile = force;
+  if (tile < 0) {
+    const int64_t t256 = ((int64_t)c.M + 255) / 256 * (((int64_t)c.N + 255) / 256);
+    const int64_t t128 = ((int64_t)c.M + 127) / 128 * (((int64_t)c.N + 127) / 128);
+    tile = t256 >= cus ? 0 : c.M > 64 && t128 >= cus / 4 ? 2 : c.M > 16 ? 4 : 5;
+  }
+  if (tile < 4 && !tiled) tile = 4;
+  if (tile < 3 && !fp8_direct(c)) tile = 3;
+  if (tile == 0 && !(c.fast_sums && c.b_rows == 128)) tile = 1;
+  return tile;
+}
+
+hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, int force, hipStream_t s) {
+  const int tile = fp8_tile(c, cus, force);
+  if (tile < 4) return launch_fp8_tile(c, tile, s);
+  return tile == 4 ? launch_ksplit<4, 2>(c, s) : launch_ksplit<1, 1>(c, s);
 }
 
 }  // namespace lasg

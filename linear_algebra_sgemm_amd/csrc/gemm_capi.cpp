@@ -55,6 +55,7 @@ std::atomic<int> g_force_sgemm_tile{-1};
 std::atomic<int> g_force_hgemm_tile{-1};
 std::atomic<int> g_force_sgemm_splits{-1};
 std::atomic<int> g_force_half_splits{-1};
+std::atomic<int> g_force_fp8_tile{-1};
 
 thread_local char t_last_error[256] = "";
 
@@ -358,6 +359,7 @@ namespace lasg {
 bool library_ready() { return g_ready.load() != 0; }
 int library_cus() { return g_cus.load(); }
 int library_hip_failure(hipError_t e) { return hip_failure(e); }
+int library_force_fp8_tile() { return g_force_fp8_tile.load(); }
 
 }  // namespace lasg
 
@@ -622,10 +624,12 @@ const char* gemm_status_string(int status) {
 }
 
 int gemm_debug_force_tile(int op, int tile) {
-  if (op != 0 && op != 1) return GEMM_STATUS_INVALID_VALUE;
-  const int count = op == 0 ? lasg::kSgemmTileCount : lasg::kHgemmTileCount;
+  if (op < 0 || op > 2) return GEMM_STATUS_INVALID_VALUE;
+  const int count = op == 0   ? lasg::kSgemmTileCount
+                    : op == 1 ? lasg::kHgemmTileCount
+                              : lasg::kFp8TileCount;
   if (tile < -1 || tile >= count) return GEMM_STATUS_INVALID_VALUE;
-  (op == 0 ? g_force_sgemm_tile : g_force_hgemm_tile).store(tile);
+  (op == 0 ? g_force_sgemm_tile : op == 1 ? g_force_hgemm_tile : g_force_fp8_tile).store(tile);
   return GEMM_STATUS_SUCCESS;
 }
 

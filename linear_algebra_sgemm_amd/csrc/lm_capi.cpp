@@ -78,7 +78,8 @@ int fp8_gemm_bias_act(int M, int N, int K, float alpha, const uint8_t* A, int ld
   if (empty) return GEMM_STATUS_SUCCESS;
   const lasg::Fp8Call c{M, N, reads_ab ? K : 0, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_rows,
                         bias, act, type, C, ldc, fast_sums == 1};
-  return finish(lasg::launch_fp8_gemm(c, lasg::library_cus(), stream));
+  return finish(
+      lasg::launch_fp8_gemm(c, lasg::library_cus(), lasg::library_force_fp8_tile(), stream));
 }
 
 int moe_ffn_workspace(const moe_shape_t* shape, size_t* bytes) {

@@ -30,17 +30,39 @@ __device__ __forceinline__ u32x4 load16(const void* p) {
   return *static_cast<const u32x4_any*>(p);
 }
 
-// 16 bytes at p of which the first `valid` (any number; <= 0 none, >= 16 all)
-// exist; the rest come back as zeros and are not read.
-__device__ __forceinline__ u32x4 load16_upto(const uint8_t* p, int valid) {
-  if (valid >= 16) return load16(p);
-  u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (e < valid) v[e / 4] |= (uint32_t)p[e] << (8 * (e % 4));
-  return v;
+// Bytes [at, at + 16) of a row of `bytes` bytes, zeros from its end on (at < 2^31 -
+// 16; the row itself may start anywhere).  Nothing past the row is read: a chunk
+// that crosses the end is the row's last 16 bytes, shifted; one wide load either
+// way, and single bytes only in rows shorter than that.
+__device__ __forceinline__ u32x4 load16_row(const void* row, int at, int bytes) {
+  const uint8_t* p = static_cast<const uint8_t*>(row);
+  if (bytes < 16) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int e = 0; e < 16 && at + e < bytes; ++e) {
+      const uint32_t b = (uint32_t)p[at + e] << (8 * (e % 4));
+      v[0] |= e / 4 == 0 ? b : 0u;
+      v[1] |= e / 4 == 1 ? b : 0u;
+      v[2] |= e / 4 == 2 ? b : 0u;
+      v[3] |= e / 4 == 3 ? b : 0u;
+    }
+    return v;
+  }
+  const int from = at < bytes - 16 ? at : bytes - 16;
+  const u32x4 v = load16(p + from);
+  const int shift = 8 * (at - from < 16 ? at - from : 16);
+  uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+  if (shift >= 64) {
+    lo = shift < 128 ? hi >> (shift - 64) : 0;
+    hi = 0;
+  } else if (shift > 0) {
+    lo = lo >> shift | hi << (64 - shift);
+    hi >>= shift;
+  }
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
-// The same in 16-bit elements (`valid` counts elements).
+// Eight 16-bit elements at p of which the first `valid` (any number; <= 0 none)
+// exist; the rest come back as zeros and are not read.
 __device__ __forceinline__ u32x4 load8h_upto(const uint16_t* p, int valid) {
   if (valid >= 8) return load16(p);
   u32x4 v = {0u, 0u, 0u, 0u};

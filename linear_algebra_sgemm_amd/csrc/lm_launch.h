@@ -17,6 +17,7 @@ namespace lasg {
 bool library_ready();
 int library_cus();
 int library_hip_failure(hipError_t e);
+int library_force_fp8_tile();   // gemm_debug_force_tile(2, ...)
 
 struct QuantizeCall {
   int rows, cols, type;
@@ -53,7 +54,14 @@ struct Fp8Call {
   int ldc;
   bool fast_sums;
 };
-hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, hipStream_t s);
+// Output tile: 0 = 128 x 256 (fast sums and one scale per 128 rows of B only), 1 =
+// 256 x 128, 2 = 128 x 128, copied straight into LDS; 3 = 128 x 128 for other
+// operands; 4 = 64 x 32 and 5 = 16 x 16 with K split over a workgroup's waves.
+constexpr int kFp8TileCount = 6;
+// The tile that runs for a call on `cus` compute units: `force`, or by shape
+// where that is -1; resolved to one that applies.
+int fp8_tile(const Fp8Call& c, int cus, int force);
+hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, int force, hipStream_t s);
 
 struct MoeCall {
   moe_shape_t shape;

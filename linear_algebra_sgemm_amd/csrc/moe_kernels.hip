@@ -118,31 +118,35 @@ struct WeightBlock {
   static __device__ __forceinline__ int column(int t, int g) {
     return FP8 ? 64 * (t / 2) + 16 * g + 8 * (t % 2) : 32 * t + 8 * g;
   }
-  __device__ __forceinline__ void load(const void* row, int64_t k0, int g, int valid) {
+  // Columns k0 .. k0 + 127 of a row of `cols`.
+  __device__ __forceinline__ void load(const void* row, int k0, int g, int cols) {
+    const uint8_t* b = static_cast<const uint8_t*>(row);
     if constexpr (FP8) {
-      const uint8_t* b = static_cast<const uint8_t*>(row) + k0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const u32x4 c = valid >= kBlockK ? load16(b + 64 * u + 16 * g)
-                                         : load16_upto(b + 64 * u + 16 * g, valid - 64 * u - 16 * g);
+        const int at = k0 + 64 * u + 16 * g;
+        const u32x4 c = cols - k0 >= kBlockK ? load16(b + at) : load16_row(b, at, cols);
         v[2 * u] = E::widen(c[0], c[1]);
         v[2 * u + 1] = E::widen(c[2], c[3]);
       }
     } else {
-      const uint16_t* b = static_cast<const uint16_t*>(row) + k0;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        v[t] = __builtin_bit_cast(typename E::vec8,
-                                  valid >= kBlockK ? load16(b + column(t, g))
-                                                   : load8h_upto(b + column(t, g), valid - column(t, g)));
+      for (int t = 0; t < 4; ++t) {
+        const int at = 2 * (k0 + column(t, g));
+        v[t] = __builtin_bit_cast(typename E::vec8, cols - k0 >= kBlockK
+                                                        ? load16(b + at)
+                                                        : load16_row(b, at, 2 * cols));
+      }
     }
   }
 };
 
+// Columns col .. col + 7 of a row of `cols`, in the block of 128 from k0.
 template <class E>
-__device__ __forceinline__ typename E::vec8 load_x(const uint16_t* row, int col, int valid) {
-  return __builtin_bit_cast(typename E::vec8,
-                            valid >= kBlockK ? load16(row + col) : load8h_upto(row + col, valid - col));
+__device__ __forceinline__ typename E::vec8 load_x(const uint16_t* row, int k0, int col, int cols) {
+  return __builtin_bit_cast(typename E::vec8, cols - k0 >= kBlockK
+                                                  ? load16(row + k0 + col)
+                                                  : load16_row(row, 2 * (k0 + col), 2 * cols));
 }
 
 }  // namespace
@@ -273,10 +277,10 @@ __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
 #pragma unroll
     for (int i = 0; i < MF; ++i) total[side][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int kb = wave; kb < kbs; kb += 8) {
-    const int k0 = kb * kBlockK, valid = D - k0;
+    const int k0 = kb * kBlockK;
     WeightBlock<E, FP8> wb[SIDES];
 #pragma unroll
-    for (int side = 0; side < SIDES; ++side) wb[side].load(w[side], k0, g, valid);
+    for (int side = 0; side < SIDES; ++side) wb[side].load(w[side], k0, g, D);
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       if (16 * i >= rows.count) break;
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
         v[side] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : total[side][i];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const auto xv = load_x<E>(x[i] + k0, WeightBlock<E, FP8>::column(t, g), valid);
+        const auto xv = load_x<E>(x[i], k0, WeightBlock<E, FP8>::column(t, g), D);
 #pragma unroll
         for (int side = 0; side < SIDES; ++side) v[side] = E::mfma(wb[side].v[t], xv, v[side]);
       }
@@ -359,9 +363,9 @@ __global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs p) {
 #pragma unroll
   for (int i = 0; i < MF; ++i) total[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int kb = wave; kb < kbs; kb += 8) {
-    const int k0 = kb * kBlockK, valid = I - k0;
+    const int k0 = kb * kBlockK;
     WeightBlock<E, FP8> wb;
-    wb.load(w, k0, g, valid);
+    wb.load(w, k0, g, I);
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       if (16 * i >= rows.count) break;
@@ -369,8 +373,8 @@ __global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs p) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int col = WeightBlock<E, FP8>::column(t, g);
-        v = E::mfma(wb.v[t], load_x<E>(p.h_hi + h_row[i] + k0, col, valid), v);
-        v = E::mfma(wb.v[t], load_x<E>(p.h_lo + h_row[i] + k0, col, valid), v);
+        v = E::mfma(wb.v[t], load_x<E>(p.h_hi + h_row[i], k0, col, I), v);
+        v = E::mfma(wb.v[t], load_x<E>(p.h_lo + h_row[i], k0, col, I), v);
       }
       if constexpr (FP8) {
 #pragma unroll

@@ -236,6 +236,23 @@ def test_product(M, N, K, fast):
 
 
 @pytest.mark.parametrize("fast", [False, True])
+@pytest.mark.parametrize("tile", range(6))
+@pytest.mark.parametrize("M,N,K", [(256, 256, 256), (512, 384, 1152), (257, 513, 640), (70, 40, 384),
+                                   (300, 260, 393), (1, 1, 1), (130, 129, 100)])
+def test_every_tile(M, N, K, tile, fast):
+    """Every kernel on whole and ragged tiles, aligned rows and rows off 16-byte boundaries."""
+    assert lib.gemm_debug_force_tile(2, tile) == lib.STATUS_SUCCESS
+    try:
+        check_product(M, N, K, "f32", fast=fast, pad=-K % 16, seed=5)
+        check_product(M, N, K, "bf16", act=lib.ACT_GELU_TANH, b_rows=1, fast=fast, pad=-K % 16,
+                      seed=6)
+        check_product(M, N, K, "f16", fast=fast, pad=1, offset=7, alpha=0.5, bias=False, seed=7)
+        check_product(M, N, K, "f32", b_rows=1, fast=fast, pad=3, act=lib.ACT_SILU, seed=8)
+    finally:
+        lib.gemm_debug_force_tile(2, -1)
+
+
+@pytest.mark.parametrize("fast", [False, True])
 @pytest.mark.parametrize("b_rows", [1, 128])
 def test_product_wide_magnitudes(b_rows, fast):
     check_product(130, 140, 1024, "f32", b_rows=b_rows, fast=fast, spread=2.0, seed=9)

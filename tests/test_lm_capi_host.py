@@ -131,3 +131,12 @@ def test_workspace_size():
     assert layer(workspace_bytes=n - 1) == BAD
     assert lib.load_library().moe_ffn_workspace(None, ctypes.byref(ctypes.c_size_t())) == BAD
     assert lib.load_library().moe_ffn_workspace(ctypes.byref(lib.MoeShape(**SHAPE)), None) == BAD
+
+
+def test_forced_tiles():
+    for tile in range(-1, 6):
+        assert lib.gemm_debug_force_tile(2, tile) == lib.STATUS_SUCCESS
+    assert lib.gemm_debug_force_tile(2, -1) == lib.STATUS_SUCCESS
+    assert lib.gemm_debug_force_tile(2, 6) == BAD
+    assert lib.gemm_debug_force_tile(2, -2) == BAD
+    assert lib.gemm_debug_force_tile(3, 0) == BAD
