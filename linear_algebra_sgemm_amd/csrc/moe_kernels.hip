@@ -7,12 +7,18 @@
 //
 // What bounds it are the chosen experts' weights, each of which is read once:
 // the tokens that chose an expert form the rows of one small product against
-// it.  A workgroup takes an expert and 16 rows of its weight; its eight waves
+// it.  A workgroup takes an expert and 16 NF rows of its weight; its eight waves
 // split the columns, read the weight straight into MFMA operands (16x16x32,
 // the tokens as the other operand) and add their fp32 sums in LDS.  Which
-// experts there are is known on the device only: the grid has a row for every
-// (token, slot) pair or every expert, whichever is fewer, and workgroups whose
-// expert another row takes, or nobody chose, end at once.
+// experts there are is known on the device only, so the grids have a row for
+// every expert (or every token and slot, whichever is fewer, once the choice is
+// written down), and workgroups whose expert nobody chose, or another row
+// takes, end at once.
+//
+// Four launches: the logits; the first product, whose workgroups find the tokens
+// of their expert from the logits (a token chose it if fewer than top_k logits come
+// before it, which is one comparison per expert, lane and token); the second
+// product; the weights w and the sum over a token's slots.
 //
 // The logits are summed in 64 bits: two experts' logits can lie closer than
 // fp32 sums of a few thousand terms resolve, and the choice between them is an
@@ -79,75 +85,170 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
-// The tokens that chose a grid row's expert, in token order: `pair[i]` is
-// token * top_k + slot.  Lane t of every wave looks at token t.
+// Whether expert o with logit u comes before expert e with logit v: NaN first,
+// then larger logits, then lower numbers (a total order whatever the logits).
+__device__ __forceinline__ bool before(double u, int o, double v, int e) {
+  const bool un = u != u, vn = v != v;
+  return un || vn ? un && (!vn || o < e) : u > v || (u == v && o < e);
+}
+
+// The tokens that chose `expert`, from the logits, in token order: pair[i] =
+// token * top_k + slot.  Returns their number.  Wave w looks at the tokens w, w + 8,
+// ... (eight at most, their loads in flight together).
+__device__ __forceinline__ int rows_from_logits(const MoeArgs& p, int expert, int* pair, int* slots) {
+  constexpr int PER_WAVE = kMaxTokens / 8;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  double own[PER_WAVE];
+  int place[PER_WAVE] = {};
+#pragma unroll
+  for (int i = 0; i < PER_WAVE; ++i)
+    if (wave + 8 * i < p.tokens)
+      own[i] = p.logits[(int64_t)(wave + 8 * i) * p.experts + expert];
+  for (int o = lane; o < p.experts + lane; o += kWave) {   // (every lane takes part in the ballots)
+    double u[PER_WAVE];
+#pragma unroll
+    for (int i = 0; i < PER_WAVE; ++i)
+      if (wave + 8 * i < p.tokens)
+        u[i] = o < p.experts ? p.logits[(int64_t)(wave + 8 * i) * p.experts + o] : 0.0;
+#pragma unroll
+    for (int i = 0; i < PER_WAVE; ++i)
+      if (wave + 8 * i < p.tokens)
+        place[i] += __popcll(__ballot(o < p.experts && before(u[i], o, own[i], expert)));
+  }
+#pragma unroll
+  for (int i = 0; i < PER_WAVE; ++i)
+    if (lane == 0 && wave + 8 * i < p.tokens) slots[wave + 8 * i] = place[i];
+  __syncthreads();
+  const bool chose = lane < p.tokens && slots[lane] < p.top_k;
+  const uint64_t mask = __ballot(chose);
+  if (wave == 0 && chose)
+    pair[__popcll(mask & ((uint64_t(1) << lane) - 1))] = lane * p.top_k + slots[lane];
+  __syncthreads();
+  return __popcll(mask);
+}
+
+// The same from the written choice, for a grid row that stands for an expert, or
+// for a (token, slot) pair: then the expert's first pair does the work.
 struct Rows {
   int expert, count;   // count == 0: nothing for this workgroup
 };
-__device__ __forceinline__ Rows find_rows(const MoeArgs& p, int grid_row, int* pair) {
+__device__ __forceinline__ Rows rows_from_ids(const MoeArgs& p, int grid_row, int* pair) {
   const int lane = threadIdx.x % kWave;
-  Rows out;
-  out.expert = p.by_expert ? grid_row : p.ids[grid_row];
-  int slot = -1;
-  if (lane < p.tokens) {
-    const int* ids = p.ids + lane * p.top_k;
-    for (int s = 0; s < p.top_k; ++s)
-      if (ids[s] == out.expert) slot = s;
+  const int pairs = p.tokens * p.top_k;
+  Rows out{p.by_expert ? grid_row : p.ids[grid_row], 0};
+  for (int q0 = 0; q0 < pairs; q0 += 4 * kWave) {   // (pairs are in token order)
+    int id[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int q = q0 + u * kWave + lane;
+      id[u] = q < pairs ? p.ids[q] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint64_t mask = __ballot(id[u] == out.expert);
+      if (mask == 0) continue;
+      if (!p.by_expert && out.count == 0 &&
+          q0 + u * kWave + __ffsll((unsigned long long)mask) - 1 != grid_row)
+        return Rows{out.expert, 0};
+      if (threadIdx.x < kWave && id[u] == out.expert)
+        pair[out.count + __popcll(mask & ((uint64_t(1) << lane) - 1))] = q0 + u * kWave + lane;
+      out.count += __popcll(mask);
+    }
   }
-  const uint64_t mask = __ballot(slot >= 0);
-  out.count = __popcll(mask);
-  const int mine = lane * p.top_k + slot;
-  if (!p.by_expert && out.count > 0) {
-    // The pair of the first token that chose the expert does the work.
-    const int first = __shfl(mine, __ffsll((unsigned long long)mask) - 1);
-    if (first != grid_row) out.count = 0;
-  }
-  if (out.count == 0) return out;
-  if (threadIdx.x < kWave && slot >= 0)
-    pair[__popcll(mask & ((uint64_t(1) << lane) - 1))] = mine;
-  __syncthreads();
+  if (out.count > 0) __syncthreads();
   return out;
 }
 
-// 128 columns of 16 rows of a weight as the first operands of four MFMAs; the
-// order of the columns depends on how the type is loaded (16 bytes a lane), and
-// `column` gives the first of the eight that MFMA t of lane group g multiplies.
+// How a lane reads a block of 128 columns: in chunks of 16 bytes of a weight's
+// row (8 or 16 columns), chunk u of lane group g at column chunk(u, g), as the
+// first operands of four MFMAs; MFMA t multiplies eight columns of chunk t / PER.
+//
+// The last, shorter block of a row (Tail): a chunk that crosses the row's end is
+// moved back to the row's last columns, and `mask` keeps those of them that no
+// other chunk covers, in weight and tokens alike (a masked infinity must not
+// meet a zero).  Rows shorter than a chunk are gathered by element.
 template <class E, bool FP8>
-struct WeightBlock {
-  typename E::vec8 v[4];
-  static __device__ __forceinline__ int column(int t, int g) {
-    return FP8 ? 64 * (t / 2) + 16 * g + 8 * (t % 2) : 32 * t + 8 * g;
-  }
-  // Columns k0 .. k0 + 127 of a row of `cols`.
-  __device__ __forceinline__ void load(const void* row, int k0, int g, int cols) {
-    const uint8_t* b = static_cast<const uint8_t*>(row);
-    if constexpr (FP8) {
+struct Block {
+  static constexpr int COLS = FP8 ? 16 : 8, CHUNKS = FP8 ? 2 : 4, PER = 4 / CHUNKS;
+  typedef typename E::vec8 vec8;
+  static __device__ __forceinline__ int chunk(int u, int g) { return FP8 ? 64 * u + 16 * g : 32 * u + 8 * g; }
+
+  struct Tail {
+    int at[CHUNKS];        // first column
+    u32x4 mask[4];         // of the eight columns of MFMA t, 16 bits each
+    u32x4 mask8[CHUNKS];   // e4m3: of the chunk's 16 bytes
+    int tiny;              // the row's columns, if fewer than a chunk (else 0)
+    __device__ __forceinline__ Tail(int k0, int cols, int g) {
+      tiny = cols < COLS ? cols : 0;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int at = k0 + 64 * u + 16 * g;
-        const u32x4 c = cols - k0 >= kBlockK ? load16(b + at) : load16_row(b, at, cols);
-        v[2 * u] = E::widen(c[0], c[1]);
-        v[2 * u + 1] = E::widen(c[2], c[3]);
-      }
-    } else {
+      for (int u = 0; u < CHUNKS; ++u) {
+        const int first = k0 + chunk(u, g);
+        at[u] = tiny ? 0 : first < cols - COLS ? first : cols - COLS;
+        // Columns at[u] + c count if they are not before `first` (nor past the end).
+        const int from = first - at[u], to = tiny ? (first == 0 ? cols : 0) : COLS;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int at = 2 * (k0 + column(t, g));
-        v[t] = __builtin_bit_cast(typename E::vec8, cols - k0 >= kBlockK
-                                                        ? load16(b + at)
-                                                        : load16_row(b, at, 2 * cols));
+        for (int x = 0; x < PER; ++x)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const int c = 8 * x + 2 * d;
+            mask[u * PER + x][d] = (c >= from && c < to ? 0xffffu : 0u) |
+                                   (c + 1 >= from && c + 1 < to ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m |= 4 * d + e >= from && 4 * d + e < to ? 0xffu << (8 * e) : 0u;
+          mask8[u][d] = m;
+        }
       }
     }
+  };
+
+  vec8 v[4];
+  __device__ __forceinline__ void set(int u, u32x4 c) {
+    if constexpr (FP8) {
+      v[2 * u] = E::widen(c[0], c[1]);
+      v[2 * u + 1] = E::widen(c[2], c[3]);
+    } else {
+      v[u] = __builtin_bit_cast(vec8, c);
+    }
+  }
+  __device__ __forceinline__ void load(const uint8_t* row, int k0, int g) {
+#pragma unroll
+    for (int u = 0; u < CHUNKS; ++u) set(u, load16(row + (k0 + chunk(u, g)) * (FP8 ? 1 : 2)));
+  }
+  __device__ __forceinline__ void load(const uint8_t* row, const Tail& tail) {
+#pragma unroll
+    for (int u = 0; u < CHUNKS; ++u) {
+      const u32x4 c = tail.tiny ? gather(row, tail.tiny * (FP8 ? 1 : 2))
+                                : load16(row + tail.at[u] * (FP8 ? 1 : 2));
+      set(u, c & (FP8 ? tail.mask8[u] : tail.mask[u]));
+    }
+  }
+  static __device__ __forceinline__ vec8 tokens(const uint16_t* row, int k0, int g, int t) {
+    return __builtin_bit_cast(vec8, load16(row + k0 + chunk(t / PER, g) + 8 * (t % PER)));
+  }
+  static __device__ __forceinline__ vec8 tokens(const uint16_t* row, const Tail& tail, int t) {
+    const int at = tail.at[t / PER] + 8 * (t % PER);
+    const u32x4 c = tail.tiny ? gather(reinterpret_cast<const uint8_t*>(row + at), 2 * (tail.tiny - at))
+                              : load16(row + at);
+    return __builtin_bit_cast(vec8, c & tail.mask[t]);
+  }
+  // The first `bytes` (fewer than 32) bytes of a row, up to 16.
+  static __device__ __forceinline__ u32x4 gather(const uint8_t* row, int bytes) {
+    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int e = 0; e < 16 && e < bytes; ++e) {
+      const uint64_t b = (uint64_t)row[e] << (8 * (e % 8));
+      lo |= e < 8 ? b : 0;
+      hi |= e < 8 ? 0 : b;
+    }
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
   }
 };
-
-// Columns col .. col + 7 of a row of `cols`, in the block of 128 from k0.
-template <class E>
-__device__ __forceinline__ typename E::vec8 load_x(const uint16_t* row, int k0, int col, int cols) {
-  return __builtin_bit_cast(typename E::vec8, cols - k0 >= kBlockK
-                                                  ? load16(row + k0 + col)
-                                                  : load16_row(row, 2 * (k0 + col), 2 * cols));
-}
 
 }  // namespace
 
@@ -188,141 +289,129 @@ __global__ void __launch_bounds__(256) moe_logits_kernel(MoeArgs p) {
   }
 }
 
-// One wave per token: an expert's place is the number of experts before it in
-// the order (NaN first, then larger logits, then lower numbers: a total order,
-// so the places are a permutation whatever the logits are).
-__global__ void __launch_bounds__(64) moe_route_kernel(MoeArgs p) {
-  extern __shared__ double key[];   // experts
-  __shared__ double chosen[kMaxTokens];   // by place, below top_k
-  const int lane = threadIdx.x, t = blockIdx.x;
-  double top = -__builtin_inf();
-  for (int e = lane; e < p.experts; e += kWave) {
-    key[e] = p.logits[(int64_t)t * p.experts + e];
-    top = key[e] > top ? key[e] : top;
-  }
+// Adds the eight waves' sums `total` of F fragments in LDS, in wave order
+// (waves 4 to 7 first put theirs there, waves 0 to 3 add their own, so that half
+// the space serves), and leaves them in part[0 .. 3], still to be added up.
+template <int F>
+__device__ __forceinline__ void join(const f32x4 (&total)[F], float (&part)[4][F][256], int wave,
+                                     int lane) {
+  if (wave >= 4) {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const double o = __shfl_xor(top, d);
-    top = o > top ? o : top;
+    for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(&part[wave - 4][f][4 * lane]) = total[f];
   }
   __syncthreads();
-  double sum = 0.0;
-  for (int e = lane; e < p.experts; e += kWave) sum += exp(key[e] - top);
-  sum = wave_sum(sum);
-  for (int e = lane; e < p.experts; e += kWave) {
-    const double v = key[e];
-    int place = 0;
-    for (int o = 0; o < p.experts; ++o) {
-      const double u = key[o];
-      const bool un = u != u, vn = v != v;
-      const bool before = un || vn ? un && (!vn || o < e) : u > v || (u == v && o < e);
-      place += before;
-    }
-    if (place < p.top_k) {
-      p.ids[t * p.top_k + place] = e;
-      chosen[place] = exp(v - top) / sum;
-    }
+  if (wave < 4) {
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+      *reinterpret_cast<f32x4*>(&part[wave][f][4 * lane]) += total[f];
   }
   __syncthreads();
-  if (lane < p.top_k) {
-    double total = 1.0;
-    if (p.norm) {
-      total = 0.0;
-      for (int s = 0; s < p.top_k; ++s) total += chosen[s];
-    }
-    p.w[t * p.top_k + lane] = (float)(chosen[lane] / total);
-  }
 }
 
-// h for 16 inner columns of one expert and all its tokens (at most 16 MF).
-template <class E, bool FP8, bool GATED, int MF>
+// h for 16 NF inner columns of one expert and all its tokens (at most 16 MF).
+template <class E, bool FP8, bool GATED, int MF, int NF>
 __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
   constexpr int SIDES = GATED ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) float part[8][SIDES][MF][256];
-  __shared__ int pair[kMaxTokens];
-  const Rows rows = find_rows(p, blockIdx.y, pair);
-  if (rows.count == 0) return;
+  __shared__ __attribute__((aligned(16))) float part[4][SIDES * NF * MF][256];
+  __shared__ int pair[kMaxTokens], slots[kMaxTokens];
+  const int expert = blockIdx.y;
+  const int count = rows_from_logits(p, expert, pair, slots);
+  if (count == 0) return;
+  if (blockIdx.x == 0 && (int)threadIdx.x < count) p.ids[pair[threadIdx.x]] = expert;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane % 16, g = lane / 16;
-  const int n0 = 16 * blockIdx.x;
+  const int n0 = 16 * NF * blockIdx.x;
   const int D = p.d_model, I = p.d_ff;
   const int64_t rows1 = (int64_t)SIDES * I;
   const uint16_t* x[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    const int at = 16 * i + r < rows.count ? 16 * i + r : rows.count - 1;
+    const int at = 16 * i + r < count ? 16 * i + r : count - 1;
     x[i] = p.X + (int64_t)(pair[at] / p.top_k) * p.ldx;
   }
-  const uint8_t* w[SIDES];
-  const float* scale[SIDES][4];
+  const uint8_t* w[SIDES][NF];
   const int64_t rbs = (rows1 + 127) / 128;
-  const int64_t kbs = (D + 127) / 128;
-#pragma unroll
-  for (int side = 0; side < SIDES; ++side) {
-    const int n = n0 + r < I ? n0 + r : I - 1;   // (rows past the end: never stored)
-    const int64_t row = (int64_t)rows.expert * rows1 + (int64_t)side * I + n;
-    w[side] = static_cast<const uint8_t*>(p.W1) + row * p.ld1 * (FP8 ? 1 : 2);
-    if constexpr (FP8) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int ne = n0 + 4 * g + e < I ? n0 + 4 * g + e : I - 1;
-        scale[side][e] = p.S1 + (int64_t)rows.expert * kbs * rbs + ((int64_t)side * I + ne) / 128;
-      }
-    }
-  }
-  f32x4 total[SIDES][MF];
+  const int kbs = (D + 127) / 128;
+  // Scales of a fragment's rows: the second half of W1 may start inside a block
+  // of 128 rows, so a fragment may lie in two; `edge` is its first row (of 16) in the second.
+  const float* scale[SIDES][NF];
+  int edge[SIDES][NF];
 #pragma unroll
   for (int side = 0; side < SIDES; ++side)
 #pragma unroll
-    for (int i = 0; i < MF; ++i) total[side][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = wave; kb < kbs; kb += 8) {
-    const int k0 = kb * kBlockK;
-    WeightBlock<E, FP8> wb[SIDES];
+    for (int j = 0; j < NF; ++j) {
+      const int n = n0 + 16 * j + r < I ? n0 + 16 * j + r : I - 1;   // (rows past the end: never stored)
+      w[side][j] = static_cast<const uint8_t*>(p.W1) +
+                   ((int64_t)expert * rows1 + (int64_t)side * I + n) * p.ld1 * (FP8 ? 1 : 2);
+      if constexpr (FP8) {
+        int64_t first = (int64_t)side * I + n0 + 16 * j;
+        if (first >= rows1) first = rows1 - 1;
+        scale[side][j] = p.S1 + (int64_t)expert * kbs * rbs + first / 128;
+        edge[side][j] = first / 128 + 1 < rbs ? 128 - (int)(first % 128) : 16;
+      }
+    }
+  f32x4 total[SIDES * NF * MF];
 #pragma unroll
-    for (int side = 0; side < SIDES; ++side) wb[side].load(w[side], k0, g, D);
+  for (int f = 0; f < SIDES * NF * MF; ++f) total[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  typedef Block<E, FP8> B;
+  auto block = [&](int kb, auto... tail) __attribute__((always_inline)) {
+    B wb[SIDES][NF];
+#pragma unroll
+    for (int side = 0; side < SIDES; ++side)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        if constexpr (sizeof...(tail) > 0)
+          wb[side][j].load(w[side][j], tail...);
+        else
+          wb[side][j].load(w[side][j], kb * kBlockK, g);
+      }
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-      if (16 * i >= rows.count) break;
-      f32x4 v[SIDES];
-#pragma unroll
-      for (int side = 0; side < SIDES; ++side)
-        v[side] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : total[side][i];
+      if (16 * i >= count) break;
+      typename E::vec8 xv[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const auto xv = load_x<E>(x[i], k0, WeightBlock<E, FP8>::column(t, g), D);
-#pragma unroll
-        for (int side = 0; side < SIDES; ++side) v[side] = E::mfma(wb[side].v[t], xv, v[side]);
+        if constexpr (sizeof...(tail) > 0)
+          xv[t] = B::tokens(x[i], tail..., t);
+        else
+          xv[t] = B::tokens(x[i], kb * kBlockK, g, t);
       }
 #pragma unroll
-      for (int side = 0; side < SIDES; ++side) {
-        if constexpr (FP8) {
+      for (int side = 0; side < SIDES; ++side)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            total[side][i][e] =
-                __builtin_fmaf(v[side][e], scale[side][e][kb * rbs], total[side][i][e]);
-        } else {
-          total[side][i] = v[side];
+        for (int j = 0; j < NF; ++j) {
+          f32x4& sum = total[(side * NF + j) * MF + i];
+          if constexpr (FP8) {
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v = E::mfma(wb[side][j].v[t], xv[t], v);
+            const float* s = scale[side][j] + kb * rbs;
+            const float s0 = s[0], s1 = edge[side][j] < 16 ? s[1] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sum[e] = __builtin_fmaf(v[e], 4 * g + e < edge[side][j] ? s0 : s1, sum[e]);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) sum = E::mfma(wb[side][j].v[t], xv[t], sum);
+          }
         }
-      }
     }
-  }
-#pragma unroll
-  for (int side = 0; side < SIDES; ++side)
-#pragma unroll
-    for (int i = 0; i < MF; ++i)
-      *reinterpret_cast<f32x4*>(&part[wave][side][i][4 * lane]) = total[side][i];
-  __syncthreads();
-  for (int v = threadIdx.x; v < MF * 256; v += 512) {
-    const int i = v / 256, at = v % 256;
-    const int token = 16 * i + (at / 4) % 16, n = n0 + 4 * (at / 64) + at % 4;
-    if (token >= rows.count || n >= I) continue;
+  };
+  const int full = D / kBlockK;
+  for (int kb = wave; kb < full; kb += 8) block(kb);
+  if (full < kbs && full % 8 == wave) block(full, typename B::Tail(full * kBlockK, D, g));
+  join(total, part, wave, lane);
+  for (int v = threadIdx.x; v < NF * MF * 256; v += 512) {
+    const int f = v / 256, at = v % 256;
+    const int token = 16 * (f % MF) + (at / 4) % 16;
+    const int n = n0 + 16 * (f / MF) + 4 * (at / 64) + at % 4;
+    if (token >= count || n >= I) continue;
     float s[SIDES];
 #pragma unroll
     for (int side = 0; side < SIDES; ++side) {
-      s[side] = part[0][side][i][at];
-#pragma unroll
-      for (int q = 1; q < 8; ++q) s[side] += part[q][side][i][at];
+      const int q = side * NF * MF + f;
+      s[side] = (part[0][q][at] + part[1][q][at]) + (part[2][q][at] + part[3][q][at]);
     }
     float h = apply_act(s[0], p.act);
     if constexpr (GATED) h *= s[SIDES - 1];
@@ -335,17 +424,17 @@ __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
   }
 }
 
-// w h W2 of 16 output columns of one expert and all its tokens, per pair.
-template <class E, bool FP8, int MF>
+// h W2 of 16 NF output columns of one expert and all its tokens, per pair.
+template <class E, bool FP8, int MF, int NF>
 __global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs p) {
-  __shared__ __attribute__((aligned(16))) float part[8][MF][256];
+  __shared__ __attribute__((aligned(16))) float part[4][NF * MF][256];
   __shared__ int pair[kMaxTokens];
-  const Rows rows = find_rows(p, blockIdx.y, pair);
+  const Rows rows = rows_from_ids(p, blockIdx.y, pair);
   if (rows.count == 0) return;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane % 16, g = lane / 16;
-  const int n0 = 16 * blockIdx.x;
+  const int n0 = 16 * NF * blockIdx.x;
   const int D = p.d_model, I = p.d_ff;
   int64_t h_row[MF];
 #pragma unroll
@@ -353,89 +442,164 @@ __global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs p) {
     const int at = 16 * i + r < rows.count ? 16 * i + r : rows.count - 1;
     h_row[i] = pair[at] * p.ldh;
   }
-  const int n = n0 + r < D ? n0 + r : D - 1;
-  const uint8_t* w = static_cast<const uint8_t*>(p.W2) +
-                     ((int64_t)rows.expert * D + n) * p.ld2 * (FP8 ? 1 : 2);
-  const int64_t rbs = (D + 127) / 128;
-  const int64_t kbs = (I + 127) / 128;
-  const float* scale = FP8 ? p.S2 + rows.expert * kbs * rbs + n0 / 128 : nullptr;
-  f32x4 total[MF];
+  const uint8_t* w[NF];
 #pragma unroll
-  for (int i = 0; i < MF; ++i) total[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = wave; kb < kbs; kb += 8) {
-    const int k0 = kb * kBlockK;
-    WeightBlock<E, FP8> wb;
-    wb.load(w, k0, g, I);
+  for (int j = 0; j < NF; ++j) {
+    const int n = n0 + 16 * j + r < D ? n0 + 16 * j + r : D - 1;
+    w[j] = static_cast<const uint8_t*>(p.W2) +
+           ((int64_t)rows.expert * D + n) * p.ld2 * (FP8 ? 1 : 2);
+  }
+  const int64_t rbs = (D + 127) / 128;
+  const int kbs = (I + 127) / 128;
+  // (16 NF divides 128: one scale for all the rows)
+  const float* scale = FP8 ? p.S2 + rows.expert * kbs * rbs + n0 / 128 : nullptr;
+  f32x4 total[NF * MF];
+#pragma unroll
+  for (int f = 0; f < NF * MF; ++f) total[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  typedef Block<E, FP8> B;
+  auto block = [&](int kb, auto... tail) __attribute__((always_inline)) {
+    B wb[NF];
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      if constexpr (sizeof...(tail) > 0)
+        wb[j].load(w[j], tail...);
+      else
+        wb[j].load(w[j], kb * kBlockK, g);
+    }
+    const float s = FP8 ? scale[kb * rbs] : 1.0f;
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       if (16 * i >= rows.count) break;
-      f32x4 v = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : total[i];
+      typename E::vec8 hi[4], lo[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int col = WeightBlock<E, FP8>::column(t, g);
-        v = E::mfma(wb.v[t], load_x<E>(p.h_hi + h_row[i], k0, col, I), v);
-        v = E::mfma(wb.v[t], load_x<E>(p.h_lo + h_row[i], k0, col, I), v);
+        if constexpr (sizeof...(tail) > 0) {
+          hi[t] = B::tokens(p.h_hi + h_row[i], tail..., t);
+          lo[t] = B::tokens(p.h_lo + h_row[i], tail..., t);
+        } else {
+          hi[t] = B::tokens(p.h_hi + h_row[i], kb * kBlockK, g, t);
+          lo[t] = B::tokens(p.h_lo + h_row[i], kb * kBlockK, g, t);
+        }
       }
-      if constexpr (FP8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          total[i][e] = __builtin_fmaf(v[e], scale[kb * rbs], total[i][e]);
-      } else {
-        total[i] = v;
+      for (int j = 0; j < NF; ++j) {
+        f32x4& sum = total[j * MF + i];
+        f32x4 v = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          v = E::mfma(wb[j].v[t], lo[t], v);
+          v = E::mfma(wb[j].v[t], hi[t], v);
+        }
+        if constexpr (FP8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(v[e], s, sum[e]);
+        } else {
+          sum = v;
+        }
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < MF; ++i) *reinterpret_cast<f32x4*>(&part[wave][i][4 * lane]) = total[i];
-  __syncthreads();
-  for (int v = threadIdx.x; v < MF * 256; v += 512) {
-    const int i = v / 256, at = v % 256;
-    const int token = 16 * i + (at / 4) % 16, col = n0 + 4 * (at / 64) + at % 4;
+  };
+  const int full = I / kBlockK;
+  for (int kb = wave; kb < full; kb += 8) block(kb);
+  if (full < kbs && full % 8 == wave) block(full, typename B::Tail(full * kBlockK, I, g));
+  join(total, part, wave, lane);
+  for (int v = threadIdx.x; v < NF * MF * 256; v += 512) {
+    const int f = v / 256, at = v % 256;
+    const int token = 16 * (f % MF) + (at / 4) % 16;
+    const int col = n0 + 16 * (f / MF) + 4 * (at / 64) + at % 4;
     if (token >= rows.count || col >= D) continue;
-    float s = part[0][i][at];
-#pragma unroll
-    for (int q = 1; q < 8; ++q) s += part[q][i][at];
-    p.part[(int64_t)pair[token] * D + col] = p.w[pair[token]] * s;
+    p.part[(int64_t)pair[token] * D + col] =
+        (part[0][f][at] + part[1][f][at]) + (part[2][f][at] + part[3][f][at]);
   }
 }
 
-// The slots of a token added in their order (no atomics: the same bits every time).
+// A token's weights, and its slots' results added in their order (no atomics: the
+// same bits every time).  The first wave of every workgroup forms the weights
+// anew, in 64 bits; the first workgroup of a token writes them down.
 template <class E>
 __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs p) {
-  const int t = blockIdx.y;
+  __shared__ float weight[32];
+  const int t = blockIdx.y, lane = threadIdx.x;
+  if (threadIdx.x < kWave) {
+    const double* l = p.logits + (int64_t)t * p.experts;
+    const double mine = lane < p.top_k ? l[p.ids[t * p.top_k + lane]] : 0.0;
+    double top = -__builtin_inf();
+    for (int e = lane; e < p.experts; e += kWave) top = l[e] > top ? l[e] : top;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      const double o = __shfl_xor(top, d);
+      top = o > top ? o : top;
+    }
+    double sum = 0.0;
+    for (int e = lane; e < p.experts; e += kWave) sum += exp(l[e] - top);
+    sum = wave_sum(sum);
+    const double q = exp(mine - top) / sum;
+    const double total = p.norm ? wave_sum(lane < p.top_k ? q : 0.0) : 1.0;
+    if (lane < p.top_k) {
+      weight[lane] = (float)(q / total);
+      if (blockIdx.x == 0) p.w[t * p.top_k + lane] = weight[lane];
+    }
+  }
+  __syncthreads();
+  const float* part = p.part + (int64_t)t * p.top_k * p.d_model;
   for (int d = blockIdx.x * 256 + threadIdx.x; d < p.d_model; d += gridDim.x * 256) {
     float s = 0.0f;
+#pragma unroll 8
     for (int q = 0; q < p.top_k; ++q)
-      s += p.part[((int64_t)t * p.top_k + q) * p.d_model + d];
+      s = __builtin_fmaf(weight[q], part[(int64_t)q * p.d_model + d], s);
     p.Y[t * p.ldy + d] = E::bits(s);
   }
 }
 
 namespace {
 
+// Tiles of 16 NF rows: the widest that leaves two workgroups per compute unit
+// (tokens are read once per workgroup, and its start and end cost a few microseconds).
+int row_tiles(int64_t n, int64_t grid_rows, int widest, int cus) {
+  int nf = widest;
+  while (nf > 1 && (n + 16 * nf - 1) / (16 * nf) * grid_rows < 2 * cus) nf /= 2;
+  return nf;
+}
+
 template <class E, bool FP8, int MF>
-hipError_t launch_moe_rows(const MoeArgs& a, bool gated, hipStream_t s) {
-  const unsigned pairs = a.tokens * a.top_k;
-  const unsigned gy = a.by_expert ? a.experts : pairs;
+hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s) {
+  const int pairs = a.tokens * a.top_k;
+  const int rows = a.experts < pairs ? a.experts : pairs;   // experts at work, at most
   moe_logits_kernel<E><<<dim3(a.experts, (a.tokens + 3) / 4), 256, 0, s>>>(a);
-  moe_route_kernel<<<a.tokens, 64, a.experts * sizeof(double), s>>>(a);
-  const dim3 up((unsigned)(((int64_t)a.d_ff + 15) / 16), gy);
-  if (gated)
-    moe_up_kernel<E, FP8, true, MF><<<up, 512, 0, s>>>(a);
+  const auto grid = [](int n, int nf, int y) {
+    return dim3((unsigned)(((int64_t)n + 16 * nf - 1) / (16 * nf)), y);
+  };
+  const int up = row_tiles(a.d_ff, rows, gated ? 2 : 4, cus);
+  if (gated) {
+    if (up == 2)
+      moe_up_kernel<E, FP8, true, MF, 2><<<grid(a.d_ff, 2, a.experts), 512, 0, s>>>(a);
+    else
+      moe_up_kernel<E, FP8, true, MF, 1><<<grid(a.d_ff, 1, a.experts), 512, 0, s>>>(a);
+  } else {
+    if (up == 4)
+      moe_up_kernel<E, FP8, false, MF, 4><<<grid(a.d_ff, 4, a.experts), 512, 0, s>>>(a);
+    else if (up == 2)
+      moe_up_kernel<E, FP8, false, MF, 2><<<grid(a.d_ff, 2, a.experts), 512, 0, s>>>(a);
+    else
+      moe_up_kernel<E, FP8, false, MF, 1><<<grid(a.d_ff, 1, a.experts), 512, 0, s>>>(a);
+  }
+  const int down = row_tiles(a.d_model, rows, 4, cus);
+  if (down == 4)
+    moe_down_kernel<E, FP8, MF, 4><<<grid(a.d_model, 4, rows), 512, 0, s>>>(a);
+  else if (down == 2)
+    moe_down_kernel<E, FP8, MF, 2><<<grid(a.d_model, 2, rows), 512, 0, s>>>(a);
   else
-    moe_up_kernel<E, FP8, false, MF><<<up, 512, 0, s>>>(a);
-  const dim3 down((unsigned)(((int64_t)a.d_model + 15) / 16), gy);
-  moe_down_kernel<E, FP8, MF><<<down, 512, 0, s>>>(a);
+    moe_down_kernel<E, FP8, MF, 1><<<grid(a.d_model, 1, rows), 512, 0, s>>>(a);
   const unsigned blocks = (unsigned)(((int64_t)a.d_model + 255) / 256);
   moe_combine_kernel<E><<<dim3(blocks, a.tokens), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class E, bool FP8>
-hipError_t launch_moe_as(const MoeArgs& a, bool gated, hipStream_t s) {
-  if (a.tokens <= 16) return launch_moe_rows<E, FP8, 1>(a, gated, s);
-  if (a.tokens <= 32) return launch_moe_rows<E, FP8, 2>(a, gated, s);
-  return launch_moe_rows<E, FP8, 4>(a, gated, s);
+hipError_t launch_moe_as(const MoeArgs& a, bool gated, int cus, hipStream_t s) {
+  if (a.tokens <= 16) return launch_moe_rows<E, FP8, 1>(a, gated, cus, s);
+  if (a.tokens <= 32) return launch_moe_rows<E, FP8, 2>(a, gated, cus, s);
+  return launch_moe_rows<E, FP8, 4>(a, gated, cus, s);
 }
 
 }  // namespace
@@ -443,7 +607,6 @@ hipError_t launch_moe_as(const MoeArgs& a, bool gated, hipStream_t s) {
 size_t moe_workspace_bytes(const moe_shape_t& s) { return moe_layout(s).bytes; }
 
 hipError_t launch_moe(const MoeCall& c, int cus, hipStream_t s) {
-  (void)cus;
   const moe_shape_t& sh = c.shape;
   const MoeWorkspace l = moe_layout(sh);
   uint8_t* ws = static_cast<uint8_t*>(c.ws);
@@ -477,8 +640,10 @@ hipError_t launch_moe(const MoeCall& c, int cus, hipStream_t s) {
   a.part = reinterpret_cast<float*>(ws + l.part);
   const bool fp8 = sh.weight_type == GEMM_TYPE_E4M3, gated = sh.gated != 0;
   if (sh.type == GEMM_TYPE_F16)
-    return fp8 ? launch_moe_as<LmF16, true>(a, gated, s) : launch_moe_as<LmF16, false>(a, gated, s);
-  return fp8 ? launch_moe_as<LmBF16, true>(a, gated, s) : launch_moe_as<LmBF16, false>(a, gated, s);
+    return fp8 ? launch_moe_as<LmF16, true>(a, gated, cus, s)
+               : launch_moe_as<LmF16, false>(a, gated, cus, s);
+  return fp8 ? launch_moe_as<LmBF16, true>(a, gated, cus, s)
+             : launch_moe_as<LmBF16, false>(a, gated, cus, s);
 }
 
 }  // namespace lasg
