@@ -8,17 +8,18 @@
 // What bounds it are the chosen experts' weights, each of which is read once:
 // the tokens that chose an expert form the rows of one small product against
 // it.  A workgroup takes an expert and 16 NF rows of its weight; its eight waves
-// split the columns, read the weight straight into MFMA operands (16x16x32,
+// take an eighth of the columns each (consecutive ones: 7 % faster than every
+// eighth block of 128), read the weight straight into MFMA operands (16x16x32,
 // the tokens as the other operand) and add their fp32 sums in LDS.  Which
 // experts there are is known on the device only, so the grids have a row for
-// every expert (or every token and slot, whichever is fewer, once the choice is
-// written down), and workgroups whose expert nobody chose, or another row
-// takes, end at once.
+// every expert or for every token and slot, whichever is fewer, and workgroups
+// whose expert nobody chose, or another row takes, end at once.
 //
-// Four launches: the logits; the first product, whose workgroups find the tokens
-// of their expert from the logits (a token chose it if fewer than top_k logits come
-// before it, which is one comparison per expert, lane and token); the second
-// product; the weights w and the sum over a token's slots.
+// Four launches: the logits; the first product, whose workgroups find their
+// expert and its tokens from the logits (a token chose an expert if fewer than
+// top_k logits come before its own: one comparison per lane and ballot for 64
+// experts), beside workgroups that write the choice and its weights down; the
+// second product; the sum over a token's slots.  For one token the last two are one.
 //
 // The logits are summed in 64 bits: two experts' logits can lie closer than
 // fp32 sums of a few thousand terms resolve, and the choice between them is an
@@ -35,6 +36,7 @@ namespace lasg {
 namespace {
 
 constexpr int kMaxTokens = 64;   // one wave's lanes hold the tokens
+constexpr int kMaxExperts = 1024, kMaxSlots = 32;   // (as lm_capi.cpp allows)
 
 // Where the parts of the workspace lie (bytes).
 struct MoeWorkspace {
@@ -57,7 +59,7 @@ MoeWorkspace moe_layout(const moe_shape_t& s) {
 
 struct MoeArgs {
   int tokens, d_model, d_ff, experts, top_k, act;
-  bool norm, by_expert;   // by_expert: grid rows are experts, else pairs
+  bool norm, by_expert;   // by_expert: grid rows are experts, else (token, slot) pairs
   const uint16_t* X;
   int64_t ldx;
   const uint16_t* R;
@@ -94,31 +96,35 @@ __device__ __forceinline__ bool before(double u, int o, double v, int e) {
 
 // The tokens that chose `expert`, from the logits, in token order: pair[i] =
 // token * top_k + slot.  Returns their number.  Wave w looks at the tokens w, w + 8,
-// ... (eight at most, their loads in flight together).
+// ..., four of them at a time.
 __device__ __forceinline__ int rows_from_logits(const MoeArgs& p, int expert, int* pair, int* slots) {
-  constexpr int PER_WAVE = kMaxTokens / 8;
+  constexpr int BATCH = 4;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  double own[PER_WAVE];
-  int place[PER_WAVE] = {};
+#pragma unroll 1
+  for (int t0 = wave; t0 < p.tokens; t0 += 8 * BATCH) {
+    double own[BATCH];
+    int place[BATCH] = {};
 #pragma unroll
-  for (int i = 0; i < PER_WAVE; ++i)
-    if (wave + 8 * i < p.tokens)
-      own[i] = p.logits[(int64_t)(wave + 8 * i) * p.experts + expert];
-  for (int o = lane; o < p.experts + lane; o += kWave) {   // (every lane takes part in the ballots)
-    double u[PER_WAVE];
+    for (int i = 0; i < BATCH; ++i)
+      if (t0 + 8 * i < p.tokens)
+        own[i] = p.logits[(int64_t)(t0 + 8 * i) * p.experts + expert];
+#pragma unroll 1
+    for (int o = lane; o < p.experts + lane; o += kWave) {   // (every lane takes part in the ballots)
+      double u[BATCH];
 #pragma unroll
-    for (int i = 0; i < PER_WAVE; ++i)
-      if (wave + 8 * i < p.tokens)
-        u[i] = o < p.experts ? p.logits[(int64_t)(wave + 8 * i) * p.experts + o] : 0.0;
+      for (int i = 0; i < BATCH; ++i)
+        if (t0 + 8 * i < p.tokens)
+          u[i] = o < p.experts ? p.logits[(int64_t)(t0 + 8 * i) * p.experts + o] : 0.0;
 #pragma unroll
-    for (int i = 0; i < PER_WAVE; ++i)
-      if (wave + 8 * i < p.tokens)
-        place[i] += __popcll(__ballot(o < p.experts && before(u[i], o, own[i], expert)));
+      for (int i = 0; i < BATCH; ++i)
+        if (t0 + 8 * i < p.tokens)
+          place[i] += __popcll(__ballot(o < p.experts && before(u[i], o, own[i], expert)));
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (lane == 0 && t0 + 8 * i < p.tokens) slots[t0 + 8 * i] = place[i];
   }
-#pragma unroll
-  for (int i = 0; i < PER_WAVE; ++i)
-    if (lane == 0 && wave + 8 * i < p.tokens) slots[wave + 8 * i] = place[i];
   __syncthreads();
   const bool chose = lane < p.tokens && slots[lane] < p.top_k;
   const uint64_t mask = __ballot(chose);
@@ -126,6 +132,80 @@ __device__ __forceinline__ int rows_from_logits(const MoeArgs& p, int expert, in
     pair[__popcll(mask & ((uint64_t(1) << lane) - 1))] = lane * p.top_k + slots[lane];
   __syncthreads();
   return __popcll(mask);
+}
+
+// The expert in place `slot` of a token's order: lane l holds the logits of the experts
+// l, l + 64, ..., and wave w finds the places of the experts w, w + 8, ....  At most
+// kPairExperts experts.
+constexpr int kPairExperts = 256;
+__device__ __forceinline__ int expert_from_logits(const MoeArgs& p, int token, int slot, int* found) {
+  constexpr int PER_LANE = kPairExperts / kWave;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const double* logits = p.logits + (int64_t)token * p.experts;
+  double u[PER_LANE];
+#pragma unroll
+  for (int c = 0; c < PER_LANE; ++c) {
+    const int o = c * kWave + lane;
+    u[c] = o < p.experts ? logits[o] : 0.0;
+  }
+#pragma unroll
+  for (int c = 0; c < PER_LANE; ++c) {
+    if (c * kWave >= p.experts) break;
+#pragma unroll 1
+    for (int l = wave; l < kWave && c * kWave + l < p.experts; l += 8) {
+      const uint64_t bits = __builtin_bit_cast(uint64_t, u[c]);
+      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)bits, l);
+      const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(bits >> 32), l);
+      const double v = __builtin_bit_cast(double, lo | (uint64_t)hi << 32);
+      const int e = c * kWave + l;
+      int place = 0;
+#pragma unroll
+      for (int d = 0; d < PER_LANE; ++d) {
+        const int o = d * kWave + lane;
+        if (d * kWave < p.experts)
+          place += __popcll(__ballot(o < p.experts && before(u[d], o, v, e)));
+      }
+      if (place == slot && lane == 0) *found = e;
+    }
+  }
+  __syncthreads();
+  return *found;
+}
+
+// A token's choice and its weights, by one workgroup (beside the product: the
+// second product is the first to need them).
+__device__ __forceinline__ void route_token(const MoeArgs& p, int t, double* key, double* chosen) {
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  for (int e = threadIdx.x; e < p.experts; e += 512) key[e] = p.logits[(int64_t)t * p.experts + e];
+  __syncthreads();
+#pragma unroll 1
+  for (int e = wave; e < p.experts; e += 8) {
+    int place = 0;
+#pragma unroll 1
+    for (int o = lane; o < p.experts + lane; o += kWave)
+      place += __popcll(__ballot(o < p.experts && before(key[o < p.experts ? o : 0], o, key[e], e)));
+    if (place < p.top_k && lane == 0) {
+      chosen[place] = key[e];
+      p.ids[t * p.top_k + place] = e;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    // (The first place holds the largest logit.  Divided by the chosen ones' sum,
+    // the sum over all experts drops out.)
+    const double top = chosen[0];
+    const double mine = lane < p.top_k ? exp(chosen[lane] - top) : 0.0;
+    double sum = mine;
+    if (!p.norm) {
+      sum = 0.0;
+      for (int e = lane; e < p.experts; e += kWave) sum += exp(key[e] - top);
+    }
+    sum = wave_sum(sum);
+    if (lane < p.top_k) p.w[t * p.top_k + lane] = (float)(mine / sum);
+  }
+  __syncthreads();
 }
 
 // The same from the written choice, for a grid row that stands for an expert, or
@@ -252,11 +332,10 @@ struct Block {
 
 }  // namespace
 
-// Logits of one expert and four tokens per workgroup, its four waves splitting
+// Logits of one expert and TT tokens per workgroup, its four waves splitting
 // the columns; products and sums in 64 bits.
-template <class E>
+template <class E, int TT>
 __global__ void __launch_bounds__(256) moe_logits_kernel(MoeArgs p) {
-  constexpr int TT = 4;
   __shared__ double sums[4][TT];
   const int e = blockIdx.x, t0 = TT * blockIdx.y;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -313,11 +392,24 @@ template <class E, bool FP8, bool GATED, int MF, int NF>
 __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
   constexpr int SIDES = GATED ? 2 : 1;
   __shared__ __attribute__((aligned(16))) float part[4][SIDES * NF * MF][256];
-  __shared__ int pair[kMaxTokens], slots[kMaxTokens];
-  const int expert = blockIdx.y;
-  const int count = rows_from_logits(p, expert, pair, slots);
-  if (count == 0) return;
-  if (blockIdx.x == 0 && (int)threadIdx.x < count) p.ids[pair[threadIdx.x]] = expert;
+  __shared__ int pair[kMaxTokens], slots[kMaxTokens], found;
+  __shared__ double key[kMaxExperts], chosen[kMaxSlots];
+  if (blockIdx.y == gridDim.y - 1) {   // (one grid row past the experts: the tokens' choices)
+    for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) route_token(p, t, key, chosen);
+    return;
+  }
+  const int expert = p.by_expert ? blockIdx.y
+                                 : expert_from_logits(p, blockIdx.y / p.top_k,
+                                                      blockIdx.y % p.top_k, &found);
+  int count = 1;
+  if (p.tokens == 1 && !p.by_expert) {
+    if (threadIdx.x == 0) pair[0] = blockIdx.y;
+    __syncthreads();
+  } else {
+    count = rows_from_logits(p, expert, pair, slots);
+  }
+  // (By pair, an expert's first pair does the work.)
+  if (count == 0 || (!p.by_expert && pair[0] != (int)blockIdx.y)) return;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane % 16, g = lane / 16;
@@ -399,8 +491,8 @@ __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
     }
   };
   const int full = D / kBlockK;
-  for (int kb = wave; kb < full; kb += 8) block(kb);
-  if (full < kbs && full % 8 == wave) block(full, typename B::Tail(full * kBlockK, D, g));
+  for (int kb = full * wave / 8; kb < full * (wave + 1) / 8; ++kb) block(kb);
+  if (full < kbs && wave == 7) block(full, typename B::Tail(full * kBlockK, D, g));
   join(total, part, wave, lane);
   for (int v = threadIdx.x; v < NF * MF * 256; v += 512) {
     const int f = v / 256, at = v % 256;
@@ -500,8 +592,8 @@ __global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs p) {
     }
   };
   const int full = I / kBlockK;
-  for (int kb = wave; kb < full; kb += 8) block(kb);
-  if (full < kbs && full % 8 == wave) block(full, typename B::Tail(full * kBlockK, I, g));
+  for (int kb = full * wave / 8; kb < full * (wave + 1) / 8; ++kb) block(kb);
+  if (full < kbs && wave == 7) block(full, typename B::Tail(full * kBlockK, I, g));
   join(total, part, wave, lane);
   for (int v = threadIdx.x; v < NF * MF * 256; v += 512) {
     const int f = v / 256, at = v % 256;
@@ -513,41 +605,98 @@ __global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs p) {
   }
 }
 
-// A token's weights, and its slots' results added in their order (no atomics: the
-// same bits every time).  The first wave of every workgroup forms the weights
-// anew, in 64 bits; the first workgroup of a token writes them down.
+// A token's slots added in their order (no atomics: the same bits every time).
 template <class E>
 __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs p) {
-  __shared__ float weight[32];
-  const int t = blockIdx.y, lane = threadIdx.x;
-  if (threadIdx.x < kWave) {
-    const double* l = p.logits + (int64_t)t * p.experts;
-    const double mine = lane < p.top_k ? l[p.ids[t * p.top_k + lane]] : 0.0;
-    double top = -__builtin_inf();
-    for (int e = lane; e < p.experts; e += kWave) top = l[e] > top ? l[e] : top;
+  const int t = blockIdx.y, d = blockIdx.x * 256 + threadIdx.x;
+  if (d >= p.d_model) return;
+  const float* part = p.part + (int64_t)t * p.top_k * p.d_model + d;
+  const float* w = p.w + t * p.top_k;
+  float s = 0.0f;
+#pragma unroll 8
+  for (int q = 0; q < p.top_k; ++q) s = __builtin_fmaf(w[q], part[(int64_t)q * p.d_model], s);
+  p.Y[t * p.ldy + d] = E::bits(s);
+}
+
+// One token: 16 columns of Y per workgroup from all its experts.  The units of
+// work are (slot, 128 columns), wave w taking an eighth of them.  The order of the
+// sum is fixed by the shape.
+template <class E, bool FP8>
+__global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
+  __shared__ __attribute__((aligned(16))) float part[4][1][256];
+  typedef Block<E, FP8> B;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = lane % 16, g = lane / 16;
+  const int n0 = 16 * blockIdx.x;
+  const int D = p.d_model, I = p.d_ff;
+  const int n = n0 + r < D ? n0 + r : D - 1;
+  const int64_t rbs = (D + 127) / 128;
+  const int kbs = (I + 127) / 128, full = I / kBlockK;
+  const int mine = p.ids[lane < p.top_k ? lane : 0];
+  const float weight = p.w[lane < p.top_k ? lane : 0];
+  f32x4 total[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
+  auto row = [&](int s) __attribute__((always_inline)) {
+    const int expert = __builtin_amdgcn_readlane(mine, s);
+    return static_cast<const uint8_t*>(p.W2) + ((int64_t)expert * D + n) * p.ld2 * (FP8 ? 1 : 2);
+  };
+  auto add = [&](f32x4 v, int s, int kb) __attribute__((always_inline)) {
+    float f = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), s));
+    if constexpr (FP8)
+      f *= p.S2[__builtin_amdgcn_readlane(mine, s) * kbs * rbs + kb * rbs + n0 / 128];
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const double o = __shfl_xor(top, d);
-      top = o > top ? o : top;
+    for (int e = 0; e < 4; ++e) total[0][e] = __builtin_fmaf(v[e], f, total[0][e]);
+  };
+  constexpr int AHEAD = 2;   // units whose loads are in flight together
+  const int units = p.top_k * full, end = units * (wave + 1) / 8;
+  for (int u0 = units * wave / 8; u0 < end; u0 += AHEAD) {
+    B wb[AHEAD];
+    typename E::vec8 hi[AHEAD][4], lo[AHEAD][4];
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const int u = u0 + a < end ? u0 + a : end - 1;
+      const int s = u / full, kb = u % full;
+      wb[a].load(row(s), kb * kBlockK, g);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        hi[a][t] = B::tokens(p.h_hi + s * p.ldh, kb * kBlockK, g, t);
+        lo[a][t] = B::tokens(p.h_lo + s * p.ldh, kb * kBlockK, g, t);
+      }
     }
-    double sum = 0.0;
-    for (int e = lane; e < p.experts; e += kWave) sum += exp(l[e] - top);
-    sum = wave_sum(sum);
-    const double q = exp(mine - top) / sum;
-    const double total = p.norm ? wave_sum(lane < p.top_k ? q : 0.0) : 1.0;
-    if (lane < p.top_k) {
-      weight[lane] = (float)(q / total);
-      if (blockIdx.x == 0) p.w[t * p.top_k + lane] = weight[lane];
+    __builtin_amdgcn_sched_barrier(0);   // (all issued before anything waits)
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      if (u0 + a >= end) break;
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        v = E::mfma(wb[a].v[t], lo[a][t], v);
+        v = E::mfma(wb[a].v[t], hi[a][t], v);
+      }
+      add(v, (u0 + a) / full, (u0 + a) % full);
     }
   }
-  __syncthreads();
-  const float* part = p.part + (int64_t)t * p.top_k * p.d_model;
-  for (int d = blockIdx.x * 256 + threadIdx.x; d < p.d_model; d += gridDim.x * 256) {
-    float s = 0.0f;
-#pragma unroll 8
-    for (int q = 0; q < p.top_k; ++q)
-      s = __builtin_fmaf(weight[q], part[(int64_t)q * p.d_model + d], s);
-    p.Y[t * p.ldy + d] = E::bits(s);
+  if (full < kbs) {
+    const typename B::Tail tail(full * kBlockK, I, g);
+#pragma unroll 1
+    for (int s = wave; s < p.top_k; s += 8) {
+      B wb;
+      wb.load(row(s), tail);
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        v = E::mfma(wb.v[t], B::tokens(p.h_lo + s * p.ldh, tail, t), v);
+        v = E::mfma(wb.v[t], B::tokens(p.h_hi + s * p.ldh, tail, t), v);
+      }
+      add(v, s, full);
+    }
+  }
+  join(total, part, wave, lane);
+  if (threadIdx.x < 16 && n0 + (int)threadIdx.x < D) {
+    const int at = 64 * (threadIdx.x / 4) + threadIdx.x % 4;   // (column 0 of the result: the token)
+    p.Y[n0 + threadIdx.x] =
+        E::bits((part[0][0][at] + part[1][0][at]) + (part[2][0][at] + part[3][0][at]));
   }
 }
 
@@ -565,31 +714,42 @@ template <class E, bool FP8, int MF>
 hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s) {
   const int pairs = a.tokens * a.top_k;
   const int rows = a.experts < pairs ? a.experts : pairs;   // experts at work, at most
-  moe_logits_kernel<E><<<dim3(a.experts, (a.tokens + 3) / 4), 256, 0, s>>>(a);
+  if (a.tokens == 1)
+    moe_logits_kernel<E, 1><<<a.experts, 256, 0, s>>>(a);
+  else if (a.tokens == 2)
+    moe_logits_kernel<E, 2><<<a.experts, 256, 0, s>>>(a);
+  else
+    moe_logits_kernel<E, 4><<<dim3(a.experts, (a.tokens + 3) / 4), 256, 0, s>>>(a);
+  const int up_rows = a.by_expert ? a.experts : pairs;
+  const int first_rows = up_rows + 1;   // (and one for the tokens' choices)
   const auto grid = [](int n, int nf, int y) {
     return dim3((unsigned)(((int64_t)n + 16 * nf - 1) / (16 * nf)), y);
   };
   const int up = row_tiles(a.d_ff, rows, gated ? 2 : 4, cus);
   if (gated) {
     if (up == 2)
-      moe_up_kernel<E, FP8, true, MF, 2><<<grid(a.d_ff, 2, a.experts), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, true, MF, 2><<<grid(a.d_ff, 2, first_rows), 512, 0, s>>>(a);
     else
-      moe_up_kernel<E, FP8, true, MF, 1><<<grid(a.d_ff, 1, a.experts), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, true, MF, 1><<<grid(a.d_ff, 1, first_rows), 512, 0, s>>>(a);
   } else {
     if (up == 4)
-      moe_up_kernel<E, FP8, false, MF, 4><<<grid(a.d_ff, 4, a.experts), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, false, MF, 4><<<grid(a.d_ff, 4, first_rows), 512, 0, s>>>(a);
     else if (up == 2)
-      moe_up_kernel<E, FP8, false, MF, 2><<<grid(a.d_ff, 2, a.experts), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, false, MF, 2><<<grid(a.d_ff, 2, first_rows), 512, 0, s>>>(a);
     else
-      moe_up_kernel<E, FP8, false, MF, 1><<<grid(a.d_ff, 1, a.experts), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, false, MF, 1><<<grid(a.d_ff, 1, first_rows), 512, 0, s>>>(a);
+  }
+  if (a.tokens == 1) {
+    moe_down_token_kernel<E, FP8><<<grid(a.d_model, 1, 1), 512, 0, s>>>(a);
+    return hipGetLastError();
   }
   const int down = row_tiles(a.d_model, rows, 4, cus);
   if (down == 4)
-    moe_down_kernel<E, FP8, MF, 4><<<grid(a.d_model, 4, rows), 512, 0, s>>>(a);
+    moe_down_kernel<E, FP8, MF, 4><<<grid(a.d_model, 4, up_rows), 512, 0, s>>>(a);
   else if (down == 2)
-    moe_down_kernel<E, FP8, MF, 2><<<grid(a.d_model, 2, rows), 512, 0, s>>>(a);
+    moe_down_kernel<E, FP8, MF, 2><<<grid(a.d_model, 2, up_rows), 512, 0, s>>>(a);
   else
-    moe_down_kernel<E, FP8, MF, 1><<<grid(a.d_model, 1, rows), 512, 0, s>>>(a);
+    moe_down_kernel<E, FP8, MF, 1><<<grid(a.d_model, 1, up_rows), 512, 0, s>>>(a);
   const unsigned blocks = (unsigned)(((int64_t)a.d_model + 255) / 256);
   moe_combine_kernel<E><<<dim3(blocks, a.tokens), 256, 0, s>>>(a);
   return hipGetLastError();
@@ -618,7 +778,7 @@ hipError_t launch_moe(const MoeCall& c, int cus, hipStream_t s) {
   a.top_k = sh.top_k;
   a.act = sh.act;
   a.norm = sh.norm_topk != 0;
-  a.by_expert = sh.experts <= sh.tokens * sh.top_k;
+  a.by_expert = sh.experts <= sh.tokens * sh.top_k || sh.experts > kPairExperts;
   a.X = c.X;
   a.ldx = c.ldx;
   a.R = c.R;
