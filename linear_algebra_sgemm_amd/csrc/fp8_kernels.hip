@@ -33,15 +33,16 @@ struct Frag {
   u32x4 c[2];
 };
 
-__device__ __forceinline__ void load_frag(Frag& f, const uint8_t* row, int lane, int k0, int K) {
+__device__ __forceinline__ void load_frag(Frag& f, const uint8_t* row, int lane, int k0) {
   const int k = k0 + 16 * (lane / 16);
-  if (K - k0 >= kBlockK) {   // (uniform over the wave)
-    f.c[0] = load16(row + k);
-    f.c[1] = load16(row + k + 64);
-  } else {
-    f.c[0] = load16_row(row, k, K);
-    f.c[1] = load16_row(row, k + 64, K);
-  }
+  f.c[0] = load16(row + k);
+  f.c[1] = load16(row + k + 64);
+}
+// The same at the end of a row of K bytes.
+__device__ __forceinline__ void load_frag_tail(Frag& f, const uint8_t* row, int lane, int k0, int K) {
+  const int k = k0 + 16 * (lane / 16);
+  f.c[0] = load16_row(row, k, K);
+  f.c[1] = load16_row(row, k + 64, K);
 }
 
 template <bool FAST>
@@ -66,21 +67,25 @@ __device__ __forceinline__ f32x4 block_product(const Frag& x, const Frag& y) {
 
 }  // namespace
 
-// 16 MF x 16 NF output tile per workgroup, its eight waves taking the blocks of
-// K in turn (wave w: blocks w, w + 8, ...) straight from memory into MFMA
-// operands, the eight totals added in LDS at the end in wave order.  Any shape,
-// stride and alignment.  Few rows: the bytes of B bound it, every one of which
-// is read once, eight consecutive 128-byte lines of a row by the eight waves.
+// 16 MF x 16 NF output tile per workgroup, its eight waves taking an eighth of
+// the blocks of K each, straight from memory into MFMA operands, the eight
+// totals added in LDS at the end in a fixed order.  Any shape, stride and
+// alignment.  Few rows: the bytes of B bound it, every one of which is read once;
+// what matters is how many are on their way.  A wave loads GROUP blocks
+// before it multiplies the first, and with many fragments (where the registers
+// allow one block only) the next block of B while it multiplies this one.
 // ROWB: one scale per row of B (else per 128 rows: one for the tile).
 template <int MF, int NF, bool FAST, bool ROWB>
 __global__ void __launch_bounds__(512) fp8_ksplit_kernel(Fp8Call p) {
-  __shared__ __attribute__((aligned(16))) f32x4 part[8][MF * NF][kWave];
+  constexpr int GROUP = MF + NF <= 3 ? 4 : MF * NF <= 4 ? 2 : 1;
+  // (with many fragments the next block of B is loaded under this one's products)
+  __shared__ __attribute__((aligned(16))) f32x4 part[4][MF * NF][kWave];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane % 16, g = lane / 16;
   const unsigned tiles_n = ((unsigned)p.N + 16 * NF - 1) / (16 * NF);
   const unsigned tiles_m = ((unsigned)p.M + 16 * MF - 1) / (16 * MF);
-  const int kbs = (int)(((unsigned)p.K + kBlockK - 1) / kBlockK);
+  const int full = p.K / kBlockK;
   for (unsigned tm = blockIdx.y; tm < tiles_m; tm += gridDim.y)
     for (unsigned tn = blockIdx.x; tn < tiles_n; tn += gridDim.x) {
       const int64_t m0 = (int64_t)tm * 16 * MF, n0 = (int64_t)tn * 16 * NF;
@@ -109,41 +114,107 @@ __global__ void __launch_bounds__(512) fp8_ksplit_kernel(Fp8Call p) {
           sb[j][0] = p.SB + n0 / kBlockK;
         }
       }
-      f32x4 total[MF][NF];
+      f32x4 total[MF * NF];
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
+      for (int f = 0; f < MF * NF; ++f) total[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      struct Scales {
+        float a[MF], b[ROWB ? NF : 1][ROWB ? 4 : 1];
+      };
+      auto load_scales = [&](Scales& s, int kb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < NF; ++j) total[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int kb = wave; kb < kbs; kb += 8) {
-        const int k0 = kb * kBlockK;
-        Frag a[MF], b[NF];
+        for (int i = 0; i < MF; ++i) s.a[i] = sa[i][(int64_t)kb * p.ldsa];
 #pragma unroll
-        for (int j = 0; j < NF; ++j) load_frag(b[j], bp[j], lane, k0, p.K);
+        for (int j = 0; j < (ROWB ? NF : 1); ++j)
 #pragma unroll
-        for (int i = 0; i < MF; ++i) load_frag(a[i], ap[i], lane, k0, p.K);
+          for (int e = 0; e < (ROWB ? 4 : 1); ++e) s.b[j][e] = sb[j][e][(int64_t)kb * p.ldsb];
+      };
+      auto add = [&](const Frag& a, const Frag& b, const Scales& s, int i, int j)
+          __attribute__((always_inline)) {
+        // (B first: the lane then holds four columns of one row of C)
+        const f32x4 v = block_product<FAST>(b, a);
+        f32x4& t = total[i * NF + j];
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          const float si = sa[i][(int64_t)kb * p.ldsa];
+        for (int e = 0; e < 4; ++e)
+          t[e] = __builtin_fmaf(v[e], s.a[i] * s.b[ROWB ? j : 0][ROWB ? e : 0], t[e]);
+      };
+      auto multiply = [&](const Frag (&a)[MF], const Frag (&b)[NF], const Scales& s)
+          __attribute__((always_inline)) {
 #pragma unroll
-          for (int j = 0; j < NF; ++j) {
-            // (B first: the lane then holds four columns of one row of C)
-            const f32x4 v = block_product<FAST>(b[j], a[i]);
+        for (int i = 0; i < MF; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              total[i][j][e] = __builtin_fmaf(
-                  v[e], si * sb[j][ROWB ? e : 0][(int64_t)kb * p.ldsb], total[i][j][e]);
+          for (int j = 0; j < NF; ++j) add(a[i], b[j], s, i, j);
+      };
+      auto load_a = [&](Frag (&a)[MF], int k0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) load_frag(a[i], ap[i], lane, k0);
+      };
+      auto load_b = [&](Frag (&b)[NF], int k0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) load_frag(b[j], bp[j], lane, k0);
+      };
+      const int first = (int)((int64_t)full * wave / 8), end = (int)((int64_t)full * (wave + 1) / 8);
+      if constexpr (GROUP > 1) {
+        for (int kb = first; kb < end; kb += GROUP) {
+          Frag a[GROUP][MF], b[GROUP][NF];
+          Scales s[GROUP];
+#pragma unroll
+          for (int u = 0; u < GROUP; ++u) {
+            const int at = kb + u < end ? kb + u : end - 1;   // (an extra read, not used)
+            load_b(b[u], at * kBlockK);
+            load_a(a[u], at * kBlockK);
+            load_scales(s[u], at);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int u = 0; u < GROUP; ++u)
+            if (kb + u < end) multiply(a[u], b[u], s[u]);
+        }
+      } else if (first < end) {
+        Frag b[2][NF];
+        load_b(b[0], first * kBlockK);
+        // Two blocks a turn, so that the buffers of B keep their registers.
+        for (int kb = first; kb < end; kb += 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (kb + u >= end) break;
+            Frag a[MF];
+            Scales s;
+            load_a(a, (kb + u) * kBlockK);
+            load_scales(s, kb + u);
+            load_b(b[1 - u], (kb + u + 1 < end ? kb + u + 1 : kb + u) * kBlockK);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(a, b[u], s);
           }
         }
       }
+      if (full * kBlockK < p.K && wave == 7) {   // the last, shorter block
+        Scales s;
+        load_scales(s, full);
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
+        for (int j = 0; j < NF; ++j) {
+          Frag b;
+          load_frag_tail(b, bp[j], lane, full * kBlockK, p.K);
 #pragma unroll
-        for (int j = 0; j < NF; ++j) part[wave][i * NF + j][lane] = total[i][j];
+          for (int i = 0; i < MF; ++i) {
+            Frag a;
+            load_frag_tail(a, ap[i], lane, full * kBlockK, p.K);
+            add(a, b, s, i, j);
+          }
+        }
+      }
+      // Waves 4 to 7 put their totals down, waves 0 to 3 add theirs (half the space).
+      if (wave >= 4) {
+#pragma unroll
+        for (int f = 0; f < MF * NF; ++f) part[wave - 4][f][lane] = total[f];
+      }
+      __syncthreads();
+      if (wave < 4) {
+#pragma unroll
+        for (int f = 0; f < MF * NF; ++f) part[wave][f][lane] += total[f];
+      }
       __syncthreads();
       for (int f = wave; f < MF * NF; f += 8) {
-        f32x4 v = part[0][f][lane];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) v += part[w][f][lane];
+        f32x4 v = (part[0][f][lane] + part[1][f][lane]) + (part[2][f][lane] + part[3][f][lane]);
         const int64_t row = m0 + 16 * (f / NF) + r, col = n0 + 16 * (f % NF) + 4 * g;
         if (row < p.M && col < p.N) {
 #pragma unroll
@@ -189,18 +260,36 @@ int fp8_tile(const Fp8Call& c, int cus, int force) {
   if (tile < 0) {
     const int64_t t256 = ((int64_t)c.M + 255) / 256 * (((int64_t)c.N + 255) / 256);
     const int64_t t128 = ((int64_t)c.M + 127) / 128 * (((int64_t)c.N + 127) / 128);
-    tile = t256 >= cus ? 0 : c.M > 64 && t128 >= cus / 4 ? 2 : c.M > 16 ? 4 : 5;
+    // K-split tiles: 16, 32 or 64 rows, as many columns as leave a tile for most CUs.
+    const int64_t n = c.N, m = ((int64_t)c.M + 63) / 64;
+    if (t256 >= cus)
+      tile = 0;
+    else if (c.M > 64 && t128 >= cus / 4)
+      tile = 2;
+    else if (c.M > 32)
+      tile = n * m >= 32 * cus ? 3 : 6;
+    else if (c.M > 16)
+      tile = n >= 32 * cus ? 7 : 8;
+    else
+      tile = n >= 64 * cus ? 9 : 10;
   }
-  if (tile < 4 && !tiled) tile = 4;
-  if (tile < 3 && !fp8_direct(c)) tile = 3;
+  if (tile < 5 && !tiled) tile = 5;
+  if (tile < 4 && !fp8_direct(c)) tile = tile == 3 ? 5 : 4;
   if (tile == 0 && !(c.fast_sums && c.b_rows == 128)) tile = 1;
   return tile;
 }
 
 hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, int force, hipStream_t s) {
   const int tile = fp8_tile(c, cus, force);
-  if (tile < 4) return launch_fp8_tile(c, tile, s);
-  return tile == 4 ? launch_ksplit<4, 2>(c, s) : launch_ksplit<1, 1>(c, s);
+  if (tile < 5) return launch_fp8_tile(c, tile, s);
+  switch (tile) {
+    case 5: return launch_ksplit<4, 2>(c, s);
+    case 6: return launch_ksplit<4, 1>(c, s);
+    case 7: return launch_ksplit<2, 2>(c, s);
+    case 8: return launch_ksplit<2, 1>(c, s);
+    case 9: return launch_ksplit<1, 2>(c, s);
+    default: return launch_ksplit<1, 1>(c, s);
+  }
 }
 
 }  // namespace lasg

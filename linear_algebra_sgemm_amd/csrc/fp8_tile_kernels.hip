@@ -20,9 +20,11 @@
 
 namespace lasg {
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool FAST_, bool ROWB_, bool DIRECT_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, bool FAST_, bool ROWB_,
+          bool DIRECT_>
 struct Fp8Tile {
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+  static constexpr int STAGES = STAGES_;   // of LDS: K tiles that are multiplied or on their way
   static constexpr bool FAST = FAST_, ROWB = ROWB_;
   // Copies straight into LDS (rows of A and B on 16-byte boundaries, 32-bit
   // offsets), else through registers.
@@ -34,16 +36,20 @@ struct Fp8Tile {
   // stage of B is enough (refilled once the wave holds its fragments).
   static constexpr bool OWN_B = WAVES_M == 1;
   static constexpr int A_BYTES = BM * kBlockK, B_BYTES = BN * kBlockK;
-  static constexpr int B_AT = 2 * A_BYTES;
-  static constexpr int SCALES_AT = B_AT + (OWN_B ? 1 : 2) * B_BYTES;   // per stage: BM, then BN floats
+  static constexpr int B_AT = STAGES * A_BYTES;
+  static constexpr int SCALES_AT = B_AT + (OWN_B ? 1 : STAGES) * B_BYTES;   // per stage: BM, then BN floats
   static constexpr int SCALE_BYTES = 4 * (BM + BN);
-  static constexpr int LDS_BYTES = SCALES_AT + 2 * SCALE_BYTES;
+  static constexpr int LDS_BYTES = SCALES_AT + STAGES * SCALE_BYTES;
   static constexpr int A_LOADS = BM / 8 / WAVES, B_LOADS = BN / 8 / WAVES;   // per wave, 1 KiB each
   static constexpr int LOADS = A_LOADS + B_LOADS;
   static constexpr int SCALE_COPIES = (BM / 64 + BN / 64 + WAVES - 1) / WAVES;   // per wave
+  static constexpr int PER_TILE = LOADS + SCALE_COPIES;   // copies of a K tile, per wave
+  static constexpr int AHEAD = STAGES - 1;   // how far the copies run before the products
+  static_assert(STAGES == 2 || (STAGES > 2 && DIRECT && !OWN_B), "stages");
+  static_assert(AHEAD * PER_TILE <= 63, "copies on their way must fit vmcnt");
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "copies split evenly over waves");
   static_assert(WTM % 32 == 0 && WTN % 32 == 0 && (ROWB || 128 % WTN == 0), "wave tile");
-  static_assert(LDS_BYTES * 8 / WAVES <= 160 * 1024, "eight waves per compute unit");
+  static_assert(LDS_BYTES * (STAGES == 2 ? 8 / WAVES : 1) <= 160 * 1024, "LDS");
 };
 
 struct Fp8TileArgs {
@@ -65,8 +71,8 @@ __device__ __forceinline__ void copy_slot(int v, int wave, int lane, int& row, i
 // Where it puts them, in the stage of K tile number t.
 template <class T>
 __device__ __forceinline__ uint32_t copy_lds(int v, int wave, int t) {
-  return v < T::A_LOADS ? (t & 1) * T::A_BYTES + (wave * T::A_LOADS + v) * 1024
-                        : T::B_AT + (T::OWN_B ? 0 : (t & 1) * T::B_BYTES) + (wave * T::B_LOADS + v - T::A_LOADS) * 1024;
+  return v < T::A_LOADS ? t % T::STAGES * T::A_BYTES + (wave * T::A_LOADS + v) * 1024
+                        : T::B_AT + (T::OWN_B ? 0 : t % T::STAGES * T::B_BYTES) + (wave * T::B_LOADS + v - T::A_LOADS) * 1024;
 }
 
 // A pointer that is the same in every lane, in scalar registers.
@@ -130,16 +136,15 @@ __device__ __forceinline__ void add(f32x16& total, const f32x16& sum, float scal
 
 // The results of a wave, 32 rows at a time: bias and activation in registers,
 // rounded to C's type, through the wave's own piece of LDS (chunks permuted as
-// above) so that whole rows of 128 (16-bit) or 256 bytes are stored, 16 bytes a
+// above) so that whole rows of 64 to 256 bytes are stored, 16 bytes a
 // lane.  The activation and the width of C are chosen outside the loops.
-constexpr int kRegion = 32 * 64 * 4;
-
 template <class T, int ACT, bool WIDE>
 __device__ __forceinline__ void write_back(const Fp8Call& c, const f32x16 (&total)[T::FM][T::FN],
                                            uint8_t* region, int m0, int n0, int wm, int wn,
                                            int lane) {
-  static_assert(T::WTN == 64 && T::WAVES * kRegion <= T::LDS_BYTES, "staging of 64 columns");
-  constexpr int SIZE = WIDE ? 4 : 2, ROW = 64 * SIZE, CHUNKS = ROW / 16;
+  constexpr int SIZE = WIDE ? 4 : 2, ROW = T::WTN * SIZE, CHUNKS = ROW / 16;
+  constexpr int LINE = ROW >= 256 ? 1 : 256 / ROW;   // rows in a line of the LDS banks
+  static_assert(1024 % ROW == 0, "whole rows per store");
   const int l32 = lane % 32, half = lane / 32;
   const int col0 = n0 + wn * T::WTN;
   const bool f16 = c.type == GEMM_TYPE_F16;
@@ -154,7 +159,7 @@ __device__ __forceinline__ void write_back(const Fp8Call& c, const f32x16 (&tota
         bias[j][q][e] = c.bias != nullptr && col + e < c.N ? c.bias[col + e] : 0.0f;
     }
   auto slot = [](int row, int chunk) {
-    return row * ROW + 16 * (chunk ^ (WIDE ? row & 15 : (row >> 1) & 7));
+    return row * ROW + 16 * (chunk ^ (row / LINE & (CHUNKS - 1)));
   };
 #pragma unroll
   for (int i = 0; i < T::FM; ++i) {
@@ -221,13 +226,18 @@ fp8_tile_kernel(Fp8TileArgs p) {
   const int kbs = (c.K + kBlockK - 1) / kBlockK;
 
   // Scales in pieces of 64, B's first (with waves side by side its own to each
-  // wave), then A's.
+  // wave), then A's; a wave past the last piece copies that again, so that
+  // all waves have the same number of copies on their way.
+  auto scale_piece = [&](int u) __attribute__((always_inline)) {
+    constexpr int PIECES = T::BM / 64 + T::BN / 64;
+    return wave + u * T::WAVES < PIECES ? wave + u * T::WAVES : PIECES - 1;
+  };
   const float* scales[T::SCALE_COPIES];
   int64_t scale_ld[T::SCALE_COPIES];
   uint32_t scale_off[T::SCALE_COPIES];
 #pragma unroll
   for (int u = 0; u < T::SCALE_COPIES; ++u) {
-    const int piece = wave + u * T::WAVES;
+    const int piece = scale_piece(u);
     const bool b = piece < T::BN / 64;
     const int row = 64 * (b ? piece : piece - T::BN / 64) + lane;
     const int last = b ? c.N - 1 - n0 : c.M - 1 - m0, at = row < last ? row : last;
@@ -244,26 +254,24 @@ fp8_tile_kernel(Fp8TileArgs p) {
   auto block_of = [&](int t) __attribute__((always_inline)) {
     return !tail_first ? t : t == 0 ? kbs - 1 : t - 1;
   };
-  // (`l`: the lane.  Offsets are formed anew for every copy: held over the loop
-  // they would take the registers of a sum.  Rows past the end read the last.)
+  // (`l`: the lane.  Rows past the end read the last; 24 bits hold a row of the tile
+  // and, with 256 rows within 2^31 bytes, a leading dimension.)
   auto copy = [&](int t, int v, int l) __attribute__((always_inline)) {
     int row, chunk;
     copy_slot<T>(v, wave, l, row, chunk);
     const bool b = v >= T::A_LOADS;
     const int last = b ? c.N - 1 - n0 : c.M - 1 - m0;
     dma16_sbase_u((b ? b_tile : a_tile) + block_of(t) * kBlockK,
-                  (uint32_t)(row < last ? row : last) * (uint32_t)(b ? c.ldb : c.lda) + 16 * chunk,
+                  __umul24(row < last ? row : last, b ? c.ldb : c.lda) + 16 * chunk,
                   lds_base + copy_lds<T>(v, wave, t));
   };
   auto copy_scales = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < T::SCALE_COPIES; ++u) {
-      const int piece = wave + u * T::WAVES;
-      if (piece < T::BN / 64 + T::BM / 64)
-        dma4_sbase(uniform(scales[u] + block_of(t) * scale_ld[u]), scale_off[u],
-                   __builtin_amdgcn_readfirstlane(lds_base + T::SCALES_AT +
-                                                  (t & 1) * T::SCALE_BYTES + 256 * piece));
-    }
+    for (int u = 0; u < T::SCALE_COPIES; ++u)
+      dma4_sbase(uniform(scales[u] + block_of(t) * scale_ld[u]), scale_off[u],
+                 __builtin_amdgcn_readfirstlane(lds_base + T::SCALES_AT +
+                                                t % T::STAGES * T::SCALE_BYTES +
+                                                256 * scale_piece(u)));
   };
   auto copy_by_hand = [&](int t, int l) __attribute__((always_inline)) {
     constexpr int BATCH = T::LOADS % 4 == 0 ? 4 : 2;
@@ -296,26 +304,33 @@ fp8_tile_kernel(Fp8TileArgs p) {
   constexpr int BLOCKS = T::FM * T::FN;
   f32x16 sum[2] = {{}, {}};
   float scale[2] = {0.0f, 0.0f}, sa[2];
-  static_assert(BLOCKS % 2 == 0, "sums alternate over K tiles too");
+  static_assert(BLOCKS % 2 == 0 || BLOCKS == 1, "sums alternate over K tiles too");
+  constexpr bool LATE = !T::ROWB && BLOCKS > 1;   // a K tile's last block waits for the next tile
 
   // This lane's fragment chunks: (s, x) = k step, 16-byte half of the 32 bytes.
   const int swizzled = 16 * ((2 * half) ^ ((l32 >> 1) & 7));
   const uint32_t frag = l32 * kBlockK;
 
-  // K tile t; COPY: with the direct copies of the next one.
+  // K tile t; COPY: with the direct copies of tile t + AHEAD.
   auto k_tile = [&](int t, auto copy_next) __attribute__((always_inline)) {
     constexpr bool COPY = decltype(copy_next)::value;
     int l = lane;
-    asm volatile("" : "+v"(l));   // (keeps the copies' offsets in the loop)
-    // Tile t has landed, and every wave is done with tile t - 1, whose stage of A
-    // takes tile t + 1.
-    wait_vmcnt<0>();
+    // Where the registers are full the copies' offsets are formed anew each time
+    // (held over the loop they would take those of a sum).
+    if constexpr (T::OWN_B || !T::DIRECT) asm volatile("" : "+v"(l));
+    // Tile t has landed (younger copies may be on their way), and every wave is
+    // done with tile t - 1, whose stage takes tile t + AHEAD.
+    constexpr int AHEAD = T::AHEAD;
+    if constexpr (COPY)
+      wait_vmcnt<(AHEAD - 1) * T::PER_TILE>();
+    else
+      wait_vmcnt<0>();
     lds_barrier();
-    const uint8_t* a_st = lds + (t & 1) * T::A_BYTES + wm * T::WTM * kBlockK + frag;
-    const uint8_t* b_st = lds + T::B_AT + (T::OWN_B ? 0 : (t & 1) * T::B_BYTES) +
+    const uint8_t* a_st = lds + t % T::STAGES * T::A_BYTES + wm * T::WTM * kBlockK + frag;
+    const uint8_t* b_st = lds + T::B_AT + (T::OWN_B ? 0 : t % T::STAGES * T::B_BYTES) +
                           wn * T::WTN * kBlockK + frag;
     const float* sb_st = reinterpret_cast<const float*>(lds + T::SCALES_AT +
-                                                        (t & 1) * T::SCALE_BYTES) + wn * T::WTN;
+                                                        t % T::STAGES * T::SCALE_BYTES) + wn * T::WTN;
     const float* sa_st = sb_st - wn * T::WTN + T::BN + wm * T::WTM + l32;
     auto read = [&](const uint8_t* base) {
       Operand<T::FAST> o;
@@ -336,11 +351,11 @@ fp8_tile_kernel(Fp8TileArgs p) {
     for (int x = 0; x < BLOCKS; ++x) {
       const int i = x / T::FN, j = x % T::FN;
       if (j == 0) a = read(a_st + i * 32 * kBlockK);
-      if (x == 0 && !T::ROWB) {
+      if (x == 0 && LATE) {
         add<T>(total[T::FM - 1][T::FN - 1], sum[1], scale[1], nullptr);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (x == 0 && COPY) copy_scales(t + 1);
+      if (x == 0 && COPY) copy_scales(t + AHEAD);
       sum[x & 1] = Operand<T::FAST>::product(b[j], a);
       if (j == 0) sa[i & 1] = sa_st[32 * i] * sb0;
       scale[x & 1] = sa[i & 1];
@@ -350,11 +365,12 @@ fp8_tile_kernel(Fp8TileArgs p) {
       // last well before the tile's end.  By block FN - 1 a wave has read its
       // fragments of B.
       if constexpr (COPY) {
-        constexpr int FIRST = T::FN - 1, OVER = BLOCKS > 4 ? BLOCKS / 2 : BLOCKS - FIRST;
+        constexpr int FIRST = T::OWN_B ? T::FN - 1 : 0;
+        constexpr int OVER = BLOCKS > 4 ? BLOCKS / 2 : BLOCKS - FIRST;
         if (x >= FIRST && x < FIRST + OVER) {
 #pragma unroll
           for (int v = (x - FIRST) * T::LOADS / OVER; v < (x - FIRST + 1) * T::LOADS / OVER; ++v)
-            copy(t + 1, v, l);
+            copy(t + AHEAD, v, l);
         }
       }
       if (x > 0) {
@@ -363,34 +379,34 @@ fp8_tile_kernel(Fp8TileArgs p) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if constexpr (T::ROWB)   // (its scales lie in the stage)
-      add<T>(total[T::FM - 1][T::FN - 1], sum[1], scale[1], sb_st + 32 * (T::FN - 1) + 4 * half);
+    if constexpr (!LATE)   // (scales per row of B lie in the stage)
+      add<T>(total[T::FM - 1][T::FN - 1], sum[(BLOCKS - 1) & 1], scale[(BLOCKS - 1) & 1], sb_st + 32 * (T::FN - 1) + 4 * half);
     if (!T::DIRECT && t + 1 < kbs) {
       copy_scales(t + 1);
       asm volatile("" : "+v"(l));
       copy_by_hand(t + 1, l);
     }
   };
-  if (kbs > 0) {
-    copy_scales(0);
-    if (T::DIRECT && !tail_first) {
 #pragma unroll
-      for (int v = 0; v < T::LOADS; ++v) copy(0, v, lane);
+  for (int first = 0; first < T::AHEAD; ++first) {
+    if (first >= kbs) break;
+    copy_scales(first);
+    if (T::DIRECT && !(first == 0 && tail_first)) {
+#pragma unroll
+      for (int v = 0; v < T::LOADS; ++v) copy(first, v, lane);
     } else {
-      copy_by_hand(0, lane);
+      copy_by_hand(first, lane);
     }
   }
   int t = 0;
-  if constexpr (T::DIRECT) {
-    for (; t + 1 < kbs; ++t) k_tile(t, std::true_type());
-    if (t < kbs) k_tile(t, std::false_type());
-  } else {
-    for (; t < kbs; ++t) k_tile(t, std::false_type());
-  }
-  if constexpr (!T::ROWB) add<T>(total[T::FM - 1][T::FN - 1], sum[1], scale[1], nullptr);
+  if constexpr (T::DIRECT)
+    for (; t + T::AHEAD < kbs; ++t) k_tile(t, std::true_type());
+  for (; t < kbs; ++t) k_tile(t, std::false_type());
+  if constexpr (LATE) add<T>(total[T::FM - 1][T::FN - 1], sum[1], scale[1], nullptr);
 
   lds_barrier();   // every wave is done reading the stages
-  uint8_t* region = lds + wave * kRegion;
+  static_assert(T::WAVES * 32 * T::WTN * 4 <= T::LDS_BYTES, "staging of 32 rows a wave");
+  uint8_t* region = lds + wave * (32 * T::WTN * 4);
   const bool wide = c.type == GEMM_TYPE_F32;
   if (c.act == GEMM_ACT_NONE)
     wide ? write_back<T, 0, true>(c, total, region, m0, n0, wm, wn, lane)
@@ -412,13 +428,13 @@ hipError_t launch_tile(const Fp8Call& c, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, bool DIRECT>
+template <int BM, int BN, int WM, int WN, int STAGES, bool DIRECT>
 hipError_t launch_as(const Fp8Call& c, hipStream_t s) {
   if (c.fast_sums)
-    return c.b_rows == 1 ? launch_tile<Fp8Tile<BM, BN, WM, WN, true, true, DIRECT>>(c, s)
-                         : launch_tile<Fp8Tile<BM, BN, WM, WN, true, false, DIRECT>>(c, s);
-  return c.b_rows == 1 ? launch_tile<Fp8Tile<BM, BN, WM, WN, false, true, DIRECT>>(c, s)
-                       : launch_tile<Fp8Tile<BM, BN, WM, WN, false, false, DIRECT>>(c, s);
+    return c.b_rows == 1 ? launch_tile<Fp8Tile<BM, BN, WM, WN, STAGES, true, true, DIRECT>>(c, s)
+                         : launch_tile<Fp8Tile<BM, BN, WM, WN, STAGES, true, false, DIRECT>>(c, s);
+  return c.b_rows == 1 ? launch_tile<Fp8Tile<BM, BN, WM, WN, STAGES, false, true, DIRECT>>(c, s)
+                       : launch_tile<Fp8Tile<BM, BN, WM, WN, STAGES, false, false, DIRECT>>(c, s);
 }
 
 }  // namespace
@@ -430,10 +446,13 @@ bool fp8_direct(const Fp8Call& c) {
 }
 
 hipError_t launch_fp8_tile(const Fp8Call& c, int tile, hipStream_t s) {
-  if (tile == 0) return launch_tile<Fp8Tile<128, 256, 1, 4, true, false, true>>(c, s);
-  if (tile == 1) return launch_as<256, 128, 4, 2, true>(c, s);
-  if (tile == 2) return launch_as<128, 128, 2, 2, true>(c, s);
-  return launch_as<128, 128, 2, 2, false>(c, s);
+  switch (tile) {
+    case 0: return launch_tile<Fp8Tile<128, 256, 1, 4, 2, true, false, true>>(c, s);
+    case 1: return launch_as<256, 128, 4, 2, 2, true>(c, s);
+    case 2: return launch_as<128, 128, 2, 2, 2, true>(c, s);
+    case 3: return launch_as<64, 64, 2, 2, 4, true>(c, s);
+    default: return launch_as<128, 128, 2, 2, 2, false>(c, s);
+  }
 }
 
 }  // namespace lasg

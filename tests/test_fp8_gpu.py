@@ -236,9 +236,9 @@ def test_product(M, N, K, fast):
 
 
 @pytest.mark.parametrize("fast", [False, True])
-@pytest.mark.parametrize("tile", range(6))
+@pytest.mark.parametrize("tile", range(11))
 @pytest.mark.parametrize("M,N,K", [(256, 256, 256), (512, 384, 1152), (257, 513, 640), (70, 40, 384),
-                                   (300, 260, 393), (1, 1, 1), (130, 129, 100)])
+                                   (300, 260, 393), (1, 1, 1), (130, 129, 100), (60, 70, 4240)])
 def test_every_tile(M, N, K, tile, fast):
     """Every kernel on whole and ragged tiles, aligned rows and rows off 16-byte boundaries."""
     assert lib.gemm_debug_force_tile(2, tile) == lib.STATUS_SUCCESS
