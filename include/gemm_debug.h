@@ -37,10 +37,10 @@ extern "C" {
  * where the operands do not allow direct copies) and 9 = 16 x 16 tiles whose
  * eight waves split K between them (any operands; small outputs; never split
  * across workgroups).  op 2 = fp8_gemm_bias_act: 0 = 128 x 256 tiles (fast
- * sums with one scale per 128 rows of B, else 1), 1 = 256 x 128, 2 = 128 x 128 and 3
- * = 64 x 64 tiles copied straight into LDS (else 4, or 5 for 3), 4 = 128 x 128
- * tiles through registers, and tiles whose eight waves split K between them: 5 = 64 x
- * 32, 6 = 64 x 16, 7 = 32 x 32, 8 = 32 x 16, 9 = 16 x 32, 10 = 16 x 16.
+ * sums with one scale per 128 rows of B, else 1), 1 = 128 x 128 and 2 = 64 x 64
+ * tiles copied straight into LDS (else 3), 3 = 128 x 128 tiles through registers,
+ * and tiles whose eight waves split K between them: 4 = 64 x 32, 5 = 64 x 16, 6 = 32
+ * x 32, 7 = 32 x 16, 8 = 16 x 32, 9 = 16 x 16.
  * Whether the aligned fast path or the
  * bounds-checked path runs still follows the shape and alignment.  Returns
  * GEMM_STATUS_INVALID_VALUE for an unknown op or tile.  Pure host state: no

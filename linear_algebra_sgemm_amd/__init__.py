@@ -120,19 +120,34 @@ def load_library():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     if hasattr(x, "data_ptr"):
         return x.data_ptr()
+    if isinstance(x, int):
+        return int(x)
     raise TypeError("expected a device pointer (int) or a tensor, got %r" % type(x))
+
+
+_raw_stream = None   # torch's current stream on the current device, as an integer
+
+
+def _find_raw_stream():
+    """torch.cuda.current_stream() builds a Stream object, about 2 us of every call; where torch
+    offers the bare handle (as its own compiled code uses it), that is taken instead."""
+    global _raw_stream
+    import torch
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if stream is not None and device is not None and torch.cuda.is_initialized():
+        _raw_stream = lambda: stream(device())   # noqa: E731
+        return _raw_stream()
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _find_raw_stream() if _raw_stream is None else _raw_stream()
     if isinstance(stream, int):
         return stream
     if hasattr(stream, "cuda_stream"):

@@ -78,7 +78,6 @@ __device__ __forceinline__ f32x4 block_product(const Frag& x, const Frag& y) {
 template <int MF, int NF, bool FAST, bool ROWB>
 __global__ void __launch_bounds__(512) fp8_ksplit_kernel(Fp8Call p) {
   constexpr int GROUP = MF + NF <= 3 ? 4 : MF * NF <= 4 ? 2 : 1;
-  // (with many fragments the next block of B is loaded under this one's products)
   __shared__ __attribute__((aligned(16))) f32x4 part[4][MF * NF][kWave];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -242,9 +241,10 @@ hipError_t launch_ksplit(const Fp8Call& c, hipStream_t s) {
     else
       fp8_ksplit_kernel<MF, NF, true, false><<<grid, 512, 0, s>>>(c);
   } else {
-    if (c.b_rows == 1)
-      fp8_ksplit_kernel<MF, NF, false, true><<<grid, 512, 0, s>>>(c);
-    else
+    if (c.b_rows == 1) {
+      if constexpr (MF * NF < 8)   // (64 x 32 does not fit the registers: see fp8_tile)
+        fp8_ksplit_kernel<MF, NF, false, true><<<grid, 512, 0, s>>>(c);
+    } else
       fp8_ksplit_kernel<MF, NF, false, false><<<grid, 512, 0, s>>>(c);
   }
   return hipGetLastError();
@@ -252,43 +252,75 @@ hipError_t launch_ksplit(const Fp8Call& c, hipStream_t s) {
 
 }  // namespace
 
+// The rule takes the tile of the least estimated time.  Measured on 256 CUs (M 16 to
+// 4096, N 1024 to 14336, K 784 to 8192):
+//  * tiles through LDS take a time per block of K that does not depend on the
+//    shape: with at most one tile per CU 0.50 (64 x 64), 0.93 (128 x 128) and 1.25
+//    us (128 x 256), with two 0.55, 1.09 and 1.80, summed as bfloat16 0.65 and
+//    1.53, then 0.70 and 2.10; more tiles than two per CU in proportion;
+//  * K-split tiles of m x n take (m + n) K bytes through a CU's load path at 23
+//    bytes a nanosecond.
+// So 24 x 4096 x 4096 runs 32 x 16 K-split tiles (9.4 us; 64 x 64: 15.5), 64 x
+// 14336 x 4096 the 64 x 64 ones (17; K-split 31), 1000 x 3000 x 777 and up to a few
+// tiles per CU 64 x 64 or 128 x 128 (the same there), 4096 x 14336 x 4096 128 x 256 (230;
+// 128 x 128: 245).  Through registers a tile takes about twice its time.
 int fp8_tile(const Fp8Call& c, int cus, int force) {
+  const auto tiles = [&](int m, int n) {
+    return (((int64_t)c.M + m - 1) / m) * (((int64_t)c.N + n - 1) / n);
+  };
   // 32-bit row and tile numbers in the tiled kernels.
-  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) &&
-                     ((int64_t)c.M + 127) / 128 * (((int64_t)c.N + 127) / 128) < (1 << 22);
+  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) && tiles(64, 64) < (1 << 24);
+  const bool direct = fp8_direct(c), wide = c.fast_sums && c.b_rows == 128;
+  static const int kSplit[6][2] = {{64, 32}, {64, 16}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
   int tile = force;
   if (tile < 0) {
-    const int64_t t256 = ((int64_t)c.M + 255) / 256 * (((int64_t)c.N + 255) / 256);
-    const int64_t t128 = ((int64_t)c.M + 127) / 128 * (((int64_t)c.N + 127) / 128);
-    // K-split tiles: 16, 32 or 64 rows, as many columns as leave a tile for most CUs.
-    const int64_t n = c.N, m = ((int64_t)c.M + 63) / 64;
-    if (t256 >= cus)
-      tile = 0;
-    else if (c.M > 64 && t128 >= cus / 4)
-      tile = 2;
-    else if (c.M > 32)
-      tile = n * m >= 32 * cus ? 3 : 6;
-    else if (c.M > 16)
-      tile = n >= 32 * cus ? 7 : 8;
-    else
-      tile = n >= 64 * cus ? 9 : 10;
+    double best = 1e30;
+    const auto offer = [&](int t, double cost) {
+      if (cost < best) {
+        best = cost;
+        tile = t;
+      }
+    };
+    if (tiled) {
+      const double blocks = (double)(((int64_t)c.K + kBlockK - 1) / kBlockK) + 2;   // (start and end: two more)
+      const auto ring = [&](int m, int n, double one, double two) {
+        const double per_cu = (double)tiles(m, n) / cus;
+        return blocks * (per_cu <= 1 ? one : per_cu <= 2 ? two : two * per_cu / 2);
+      };
+      const bool fast = c.fast_sums;
+      const double t64 = ring(64, 64, fast ? 500 : 650, fast ? 550 : 700);
+      const double t128 = ring(128, 128, fast ? 930 : 1530, fast ? 1090 : 2100);
+      if (direct) {
+        if (wide) offer(0, ring(128, 256, 1250, 1800));
+        offer(1, t128);
+        offer(2, t64);
+      } else {
+        offer(3, 2 * t128);
+      }
+    }
+    for (int i = !c.fast_sums && c.b_rows == 1; i < 6; ++i) {
+      const int m = kSplit[i][0], n = kSplit[i][1];
+      const double rounds = (double)((tiles(m, n) + cus - 1) / cus);
+      offer(4 + i, rounds * (m + n) * ((double)c.K + 512) / 23);
+    }
   }
-  if (tile < 5 && !tiled) tile = 5;
-  if (tile < 4 && !fp8_direct(c)) tile = tile == 3 ? 5 : 4;
-  if (tile == 0 && !(c.fast_sums && c.b_rows == 128)) tile = 1;
+  if (tile < 4 && !tiled) tile = 4;
+  if (tile < 3 && !direct) tile = 3;
+  if (tile == 0 && !wide) tile = 1;
+  if (tile == 4 && !c.fast_sums && c.b_rows == 1) tile = 5;
   return tile;
 }
 
 hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, int force, hipStream_t s) {
   const int tile = fp8_tile(c, cus, force);
-  if (tile < 5) return launch_fp8_tile(c, tile, s);
   switch (tile) {
-    case 5: return launch_ksplit<4, 2>(c, s);
-    case 6: return launch_ksplit<4, 1>(c, s);
-    case 7: return launch_ksplit<2, 2>(c, s);
-    case 8: return launch_ksplit<2, 1>(c, s);
-    case 9: return launch_ksplit<1, 2>(c, s);
-    default: return launch_ksplit<1, 1>(c, s);
+    case 4: return launch_ksplit<4, 2>(c, s);
+    case 5: return launch_ksplit<4, 1>(c, s);
+    case 6: return launch_ksplit<2, 2>(c, s);
+    case 7: return launch_ksplit<2, 1>(c, s);
+    case 8: return launch_ksplit<1, 2>(c, s);
+    case 9: return launch_ksplit<1, 1>(c, s);
+    default: return launch_fp8_tile(c, tile, s);
   }
 }
 

@@ -303,7 +303,7 @@ fp8_tile_kernel(Fp8TileArgs p) {
 
   constexpr int BLOCKS = T::FM * T::FN;
   f32x16 sum[2] = {{}, {}};
-  float scale[2] = {0.0f, 0.0f}, sa[2];
+  float scale[2] = {0.0f, 0.0f};
   static_assert(BLOCKS % 2 == 0 || BLOCKS == 1, "sums alternate over K tiles too");
   constexpr bool LATE = !T::ROWB && BLOCKS > 1;   // a K tile's last block waits for the next tile
 
@@ -344,21 +344,25 @@ fp8_tile_kernel(Fp8TileArgs p) {
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) b[j] = read(b_st + j * 32 * kBlockK);
     const float sb0 = T::ROWB ? 1.0f : sb_st[0];
+    float sa[T::FM];
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) sa[i] = sa_st[32 * i];
+    a = read(a_st);
     // Block x's matrix instructions go out before block x - 1's sum is scaled,
     // so that the vector unit works under them; the last block of a K tile is
     // scaled in the next one, under the latency of its first reads.
 #pragma unroll
     for (int x = 0; x < BLOCKS; ++x) {
       const int i = x / T::FN, j = x % T::FN;
-      if (j == 0) a = read(a_st + i * 32 * kBlockK);
+      if (!T::DIRECT && j == 0 && i > 0) a = read(a_st + i * 32 * kBlockK);
       if (x == 0 && LATE) {
         add<T>(total[T::FM - 1][T::FN - 1], sum[1], scale[1], nullptr);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (x == 0 && COPY) copy_scales(t + AHEAD);
       sum[x & 1] = Operand<T::FAST>::product(b[j], a);
-      if (j == 0) sa[i & 1] = sa_st[32 * i] * sb0;
-      scale[x & 1] = sa[i & 1];
+      scale[x & 1] = sa[i] * sb0;
+      if (T::DIRECT && j == T::FN - 1 && i + 1 < T::FM) a = read(a_st + (i + 1) * 32 * kBlockK);
       __builtin_amdgcn_sched_barrier(0);
       // The next tile's copies, some under each block's matrix instructions (all
       // at once would hold every wave at issue for about a thousand cycles), the
@@ -442,15 +446,14 @@ hipError_t launch_as(const Fp8Call& c, hipStream_t s) {
 bool fp8_direct(const Fp8Call& c) {
   return c.lda % 16 == 0 && c.ldb % 16 == 0 && (reinterpret_cast<uintptr_t>(c.A) & 15u) == 0 &&
          (reinterpret_cast<uintptr_t>(c.B) & 15u) == 0 &&
-         (int64_t)c.lda * 256 < (int64_t(1) << 31) && (int64_t)c.ldb * 256 < (int64_t(1) << 31);
+         c.lda < (1 << 23) && c.ldb < (1 << 23);   // 256 rows within 2^31 bytes, 24-bit products
 }
 
 hipError_t launch_fp8_tile(const Fp8Call& c, int tile, hipStream_t s) {
   switch (tile) {
     case 0: return launch_tile<Fp8Tile<128, 256, 1, 4, 2, true, false, true>>(c, s);
-    case 1: return launch_as<256, 128, 4, 2, 2, true>(c, s);
-    case 2: return launch_as<128, 128, 2, 2, 2, true>(c, s);
-    case 3: return launch_as<64, 64, 2, 2, 4, true>(c, s);
+    case 1: return launch_as<128, 128, 2, 2, 2, true>(c, s);
+    case 2: return launch_as<64, 64, 2, 2, 4, true>(c, s);
     default: return launch_as<128, 128, 2, 2, 2, false>(c, s);
   }
 }
