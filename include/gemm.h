@@ -150,6 +150,7 @@ int bgemm_bias_act(int M, int N, int K, float alpha,
  * F32, F16 or BF16; the last blocks of a row or column may be shorter),
  *   Q[i][j] = x[i][j] / s, rounded to e4m3 to nearest even,
  *   S[j / 128][i] = s  (block_rows 1)  or  S[j / 128][i / 128] = s  (128),
+ * s and x / s rounded to fp32 for 16-bit X, formed in 64 bits for FP32 X,
  * Q rows x cols with leading dimension ldq >= cols, S with lds >= rows, or >=
  * ceil(rows / 128).  QT, ST: the same of the transpose of X: QT cols x rows
  * (ldqt >= rows), blocks of 128 rows of X by one column (ST[i / 128][j]) or by

@@ -10,11 +10,18 @@
 // the block become 0 and the infinities NaN), as the formula says.  The lower bound on s
 // keeps 1 / s finite; a block of zeros has s = 2^-126 and values 0.
 //
-// The quotient is formed from the block's correctly rounded reciprocal r: q0 =
-// x r, then q = q0 + r (x - q0 s) with fused multiply-adds, which is x / s
-// correctly rounded (Markstein's theorem) unless the remainder underflows, where
-// the quotient is far below e4m3's smallest value.  Three operations instead of
-// a division's ten.
+// The quotient comes from the block's correctly rounded reciprocal r: q0 = x r,
+// then q = q0 + r (x - q0 s) with fused multiply-adds, which is x / s correctly
+// rounded (Markstein's theorem) unless the remainder underflows, where the
+// quotient is far below e4m3's smallest value.  Three operations instead of a division's ten.
+// For 16-bit inputs scale and quotient are fp32 numbers.  For fp32 inputs
+// they are formed in 64 bits and rounded once: rounded twice, one or two of 4096 x
+// 4096 weights went to the wrong side of the middle between two e4m3 numbers.
+// The 64-bit quotient reaches the conversion as an fp32 number whose last bit
+// stands for everything below it, so that nothing is lost before it.  16-bit
+// inputs gain nothing from that (their quotients meet such a middle exactly or
+// stay clear of it by far more than an fp32 rounding) and pay: 4096 x 14336 both
+// ways 57 us against 81, bound by the vector unit instead of by memory.
 #include "lm_common.h"
 #include "lm_launch.h"
 
@@ -22,8 +29,8 @@ namespace lasg {
 
 namespace {
 
-constexpr float kE4m3Max = 448.0f;
-constexpr float kMinScale = 1.1754943508222875e-38f;   // 2^-126
+constexpr double kE4m3Max = 448.0;
+constexpr double kMinScale = 1.1754943508222875e-38;   // 2^-126
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
@@ -101,19 +108,40 @@ __device__ __forceinline__ uint32_t max16(uint32_t x) {
   return x;
 }
 
-// A block's scale, and what its quotients need.
+// A block's scale, and what its quotients need.  (An infinite or NaN scale takes
+// no remainder step: infinity times zero.)
+template <int TYPE>
 struct Scale {
   float s, r, sc;
   __device__ __forceinline__ explicit Scale(float amax) {
-    s = amax / kE4m3Max;
-    if (s < kMinScale) s = kMinScale;   // (false for NaN)
+    s = amax / (float)kE4m3Max;
+    if (s < (float)kMinScale) s = (float)kMinScale;   // (false for NaN)
     r = 1.0f / s;
-    // An infinite or NaN scale takes no remainder step (infinity times zero).
     sc = __builtin_fabsf(s) < __builtin_inff() ? s : 0.0f;
   }
   __device__ __forceinline__ float operator()(float x) const {
     const float q = x * r;
     return __builtin_fmaf(__builtin_fmaf(-q, sc, x), r, q);
+  }
+};
+template <>
+struct Scale<GEMM_TYPE_F32> {
+  float s;
+  double r, sc;
+  __device__ __forceinline__ explicit Scale(float amax) {
+    double s64 = (double)amax * (1.0 / kE4m3Max);
+    if (s64 < kMinScale) s64 = kMinScale;
+    s = (float)s64;
+    r = 1.0 / s64;
+    sc = s64 <= 3.5e38 ? s64 : 0.0;
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    const double q0 = (double)x * r;
+    const double q = __builtin_fma(__builtin_fma(-q0, sc, (double)x), r, q0);
+    const uint64_t bits = __builtin_bit_cast(uint64_t, q);
+    const uint32_t lo = (uint32_t)bits, below = lo & 0x1fffffffu;   // what fp32 does not hold
+    const uint32_t odd = (lo & 0xe0000000u) | (below != 0 ? 0x20000000u : 0u);
+    return (float)__builtin_bit_cast(double, (bits & 0xffffffff00000000u) | odd);
   }
 };
 
@@ -161,7 +189,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeCall p) {
         typename Eight<TYPE>::Mag m = x[i].mag(0);
 #pragma unroll
         for (int e = 1; e < Eight<TYPE>::PARTS; ++e) m = mag_max(m, x[i].mag(e));
-        const Scale sc(Eight<TYPE>::value(max16(mag_all(m))));
+        const Scale<TYPE> sc(Eight<TYPE>::value(max16(mag_all(m))));
         float q[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = sc(x[i].at(e));
@@ -247,7 +275,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantizeCall p) {
         uint32_t tile_max = maxima[0][0];
 #pragma unroll
         for (int w = 1; w < 4; ++w) tile_max = mag_max(tile_max, maxima[0][w]);
-        const Scale sc(E::value(tile_max));
+        const Scale<TYPE> sc(E::value(tile_max));
         if (tid == 0) {
           if constexpr (PLAIN) p.S[(int64_t)tn * p.lds + tm] = sc.s;
           if constexpr (TURNED) p.ST[(int64_t)tm * p.ldst + tn] = sc.s;
@@ -293,7 +321,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantizeCall p) {
         if constexpr (PLAIN) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const Scale sc(E::value(row_max[i]));
+            const Scale<TYPE> sc(E::value(row_max[i]));
             float q[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) q[e] = sc(x[i].at(e));
@@ -311,7 +339,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantizeCall p) {
             uint32_t cmax = maxima[0][8 * c + e];
 #pragma unroll
             for (int w = 1; w < 4; ++w) cmax = mag_max(cmax, maxima[w][8 * c + e]);
-            const Scale sc(E::value(cmax));
+            const Scale<TYPE> sc(E::value(cmax));
             float q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[i] = sc(x[i].at(e));

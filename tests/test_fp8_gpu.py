@@ -1,7 +1,7 @@
 """GPU tests of block quantisation and the block-scaled e4m3 product against their definitions.
 
-Quantisation is held to equality: scale and quotient are correctly rounded fp32 divisions, which the
-CPU forms too.  The product is held to a bound of its own roundings, with u = 2^-24:
+Quantisation is held to equality: scale and quotient are correctly rounded divisions, in fp32 for
+16-bit values and in 64 bits for fp32 ones, which the CPU forms too.  The product is held to a bound of its own roundings, with u = 2^-24:
   exact sums  - a block's 128 exact products are added in fp32 (at most 128 roundings), each block's
                 sum meets two roundings of its scale and one of its addition, eight partial totals are
                 added: (128 + blocks + 16) u of sum |s_a a s_b b|;
@@ -38,14 +38,19 @@ def blocks(n, of=128):
 
 
 def reference(x, b):
-    """Scales (blocks of columns first) and e4m3 values of a CPU matrix, from fp32 divisions."""
+    """Scales (blocks of columns first) and e4m3 values of a CPU matrix: scale and quotient in fp32
+    for 16-bit values, for fp32 ones in 64 bits."""
     rows, cols = x.shape
-    y = torch.zeros((blocks(rows, b) * b, blocks(cols) * 128))
-    y[:rows, :cols] = x.float()
+    wide = torch.float64 if x.dtype == torch.float32 else torch.float32
+    y = torch.zeros((blocks(rows, b) * b, blocks(cols) * 128), dtype=wide)
+    y[:rows, :cols] = x.to(wide)
     y = y.reshape(blocks(rows, b), b, blocks(cols), 128)
-    s = (y.abs().amax(dim=(1, 3)) / 448).clamp_min(2.0 ** -126)
-    q = (y / s[:, None, :, None]).reshape(blocks(rows, b) * b, -1)[:rows, :cols]
-    return q.to(E4M3), s.t().contiguous()
+    amax = y.abs().amax(dim=(1, 3))
+    s = (amax * (1.0 / 448) if wide == torch.float64 else amax / 448).clamp_min(2.0 ** -126)
+    q = (y / s[:, None, :, None]).reshape(blocks(rows, b) * b, -1)[:rows, :cols].double()
+    # Nearest multiple of e4m3's spacing at the value's size, ties to even.
+    space = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 3)
+    return (torch.round(q / space) * space).float().to(E4M3), s.float().t().contiguous()
 
 
 def run_quantize(x, b, plain=True, turned=True, pad=0, offset=0):
