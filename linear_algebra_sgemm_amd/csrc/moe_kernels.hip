@@ -95,35 +95,36 @@ __device__ __forceinline__ bool before(double u, int o, double v, int e) {
 }
 
 // The tokens that chose `expert`, from the logits, in token order: pair[i] =
-// token * top_k + slot.  Returns their number.  Wave w looks at the tokens w, w + 8,
+// token * top_k + slot.  Returns their number.  Wave w of W looks at the tokens w, w + W,
 // ..., four of them at a time.
+template <int W>
 __device__ __forceinline__ int rows_from_logits(const MoeArgs& p, int expert, int* pair, int* slots) {
   constexpr int BATCH = 4;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 #pragma unroll 1
-  for (int t0 = wave; t0 < p.tokens; t0 += 8 * BATCH) {
+  for (int t0 = wave; t0 < p.tokens; t0 += W * BATCH) {
     double own[BATCH];
     int place[BATCH] = {};
 #pragma unroll
     for (int i = 0; i < BATCH; ++i)
-      if (t0 + 8 * i < p.tokens)
-        own[i] = p.logits[(int64_t)(t0 + 8 * i) * p.experts + expert];
+      if (t0 + W * i < p.tokens)
+        own[i] = p.logits[(int64_t)(t0 + W * i) * p.experts + expert];
 #pragma unroll 1
     for (int o = lane; o < p.experts + lane; o += kWave) {   // (every lane takes part in the ballots)
       double u[BATCH];
 #pragma unroll
       for (int i = 0; i < BATCH; ++i)
-        if (t0 + 8 * i < p.tokens)
-          u[i] = o < p.experts ? p.logits[(int64_t)(t0 + 8 * i) * p.experts + o] : 0.0;
+        if (t0 + W * i < p.tokens)
+          u[i] = o < p.experts ? p.logits[(int64_t)(t0 + W * i) * p.experts + o] : 0.0;
 #pragma unroll
       for (int i = 0; i < BATCH; ++i)
-        if (t0 + 8 * i < p.tokens)
+        if (t0 + W * i < p.tokens)
           place[i] += __popcll(__ballot(o < p.experts && before(u[i], o, own[i], expert)));
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i)
-      if (lane == 0 && t0 + 8 * i < p.tokens) slots[t0 + 8 * i] = place[i];
+      if (lane == 0 && t0 + W * i < p.tokens) slots[t0 + W * i] = place[i];
   }
   __syncthreads();
   const bool chose = lane < p.tokens && slots[lane] < p.top_k;
@@ -135,9 +136,10 @@ __device__ __forceinline__ int rows_from_logits(const MoeArgs& p, int expert, in
 }
 
 // The expert in place `slot` of a token's order: lane l holds the logits of the experts
-// l, l + 64, ..., and wave w finds the places of the experts w, w + 8, ....  At most
+// l, l + 64, ..., and wave w finds the places of the experts w, w + W, ....  At most
 // kPairExperts experts.
 constexpr int kPairExperts = 256;
+template <int W>
 __device__ __forceinline__ int expert_from_logits(const MoeArgs& p, int token, int slot, int* found) {
   constexpr int PER_LANE = kPairExperts / kWave;
   const int lane = threadIdx.x % kWave;
@@ -153,7 +155,7 @@ __device__ __forceinline__ int expert_from_logits(const MoeArgs& p, int token, i
   for (int c = 0; c < PER_LANE; ++c) {
     if (c * kWave >= p.experts) break;
 #pragma unroll 1
-    for (int l = wave; l < kWave && c * kWave + l < p.experts; l += 8) {
+    for (int l = wave; l < kWave && c * kWave + l < p.experts; l += W) {
       const uint64_t bits = __builtin_bit_cast(uint64_t, u[c]);
       const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)bits, l);
       const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(bits >> 32), l);
@@ -175,13 +177,14 @@ __device__ __forceinline__ int expert_from_logits(const MoeArgs& p, int token, i
 
 // A token's choice and its weights, by one workgroup (beside the product: the
 // second product is the first to need them).
+template <int W>
 __device__ __forceinline__ void route_token(const MoeArgs& p, int t, double* key, double* chosen) {
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  for (int e = threadIdx.x; e < p.experts; e += 512) key[e] = p.logits[(int64_t)t * p.experts + e];
+  for (int e = threadIdx.x; e < p.experts; e += 64 * W) key[e] = p.logits[(int64_t)t * p.experts + e];
   __syncthreads();
 #pragma unroll 1
-  for (int e = wave; e < p.experts; e += 8) {
+  for (int e = wave; e < p.experts; e += W) {
     int place = 0;
 #pragma unroll 1
     for (int o = lane; o < p.experts + lane; o += kWave)
@@ -368,45 +371,55 @@ __global__ void __launch_bounds__(256) moe_logits_kernel(MoeArgs p) {
   }
 }
 
-// Adds the eight waves' sums `total` of F fragments in LDS, in wave order
-// (waves 4 to 7 first put theirs there, waves 0 to 3 add their own, so that half
-// the space serves), and leaves them in part[0 .. 3], still to be added up.
-template <int F>
-__device__ __forceinline__ void join(const f32x4 (&total)[F], float (&part)[4][F][256], int wave,
+// Adds the W waves' sums `total` of F fragments in LDS, in a fixed order (the
+// upper half of the waves first put theirs there, the lower half add their
+// own, so that half the space serves) and leaves them in part, still to be added up by joined().
+template <int F, int H>
+__device__ __forceinline__ void join(const f32x4 (&total)[F], float (&part)[H][F][256], int wave,
                                      int lane) {
-  if (wave >= 4) {
+  if (wave >= H) {
 #pragma unroll
-    for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(&part[wave - 4][f][4 * lane]) = total[f];
+    for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(&part[wave - H][f][4 * lane]) = total[f];
   }
   __syncthreads();
-  if (wave < 4) {
+  if (wave < H) {
 #pragma unroll
     for (int f = 0; f < F; ++f)
       *reinterpret_cast<f32x4*>(&part[wave][f][4 * lane]) += total[f];
   }
   __syncthreads();
 }
+template <int F, int H>
+__device__ __forceinline__ float joined(const float (&part)[H][F][256], int f, int at) {
+  if constexpr (H == 2) return part[0][f][at] + part[1][f][at];
+  return (part[0][f][at] + part[1][f][at]) + (part[2 % H][f][at] + part[3 % H][f][at]);
+}
+
+// Waves of a workgroup of the two products.  With many tokens a wave's sums fill
+// the registers of half a SIMD; workgroups of four waves then leave room for
+// two on a compute unit, one starting or ending while the other reads.
+constexpr int waves_of(int mf) { return mf == 4 ? 4 : 8; }
 
 // h for 16 NF inner columns of one expert and all its tokens (at most 16 MF).
 template <class E, bool FP8, bool GATED, int MF, int NF>
-__global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
-  constexpr int SIDES = GATED ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) float part[4][SIDES * NF * MF][256];
+__global__ void __launch_bounds__(64 * waves_of(MF)) moe_up_kernel(MoeArgs p) {
+  constexpr int SIDES = GATED ? 2 : 1, W = waves_of(MF);
+  __shared__ __attribute__((aligned(16))) float part[W / 2][SIDES * NF * MF][256];
   __shared__ int pair[kMaxTokens], slots[kMaxTokens], found;
   __shared__ double key[kMaxExperts], chosen[kMaxSlots];
   if (blockIdx.y == gridDim.y - 1) {   // (one grid row past the experts: the tokens' choices)
-    for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) route_token(p, t, key, chosen);
+    for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) route_token<W>(p, t, key, chosen);
     return;
   }
   const int expert = p.by_expert ? blockIdx.y
-                                 : expert_from_logits(p, blockIdx.y / p.top_k,
+                                 : expert_from_logits<W>(p, blockIdx.y / p.top_k,
                                                       blockIdx.y % p.top_k, &found);
   int count = 1;
   if (p.tokens == 1 && !p.by_expert) {
     if (threadIdx.x == 0) pair[0] = blockIdx.y;
     __syncthreads();
   } else {
-    count = rows_from_logits(p, expert, pair, slots);
+    count = rows_from_logits<W>(p, expert, pair, slots);
   }
   // (By pair, an expert's first pair does the work.)
   if (count == 0 || (!p.by_expert && pair[0] != (int)blockIdx.y)) return;
@@ -491,10 +504,10 @@ __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
     }
   };
   const int full = D / kBlockK;
-  for (int kb = full * wave / 8; kb < full * (wave + 1) / 8; ++kb) block(kb);
-  if (full < kbs && wave == 7) block(full, typename B::Tail(full * kBlockK, D, g));
+  for (int kb = full * wave / W; kb < full * (wave + 1) / W; ++kb) block(kb);
+  if (full < kbs && wave == W - 1) block(full, typename B::Tail(full * kBlockK, D, g));
   join(total, part, wave, lane);
-  for (int v = threadIdx.x; v < NF * MF * 256; v += 512) {
+  for (int v = threadIdx.x; v < NF * MF * 256; v += 64 * W) {
     const int f = v / 256, at = v % 256;
     const int token = 16 * (f % MF) + (at / 4) % 16;
     const int n = n0 + 16 * (f / MF) + 4 * (at / 64) + at % 4;
@@ -503,7 +516,7 @@ __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
 #pragma unroll
     for (int side = 0; side < SIDES; ++side) {
       const int q = side * NF * MF + f;
-      s[side] = (part[0][q][at] + part[1][q][at]) + (part[2][q][at] + part[3][q][at]);
+      s[side] = joined(part, q, at);
     }
     float h = apply_act(s[0], p.act);
     if constexpr (GATED) h *= s[SIDES - 1];
@@ -518,8 +531,9 @@ __global__ void __launch_bounds__(512) moe_up_kernel(MoeArgs p) {
 
 // h W2 of 16 NF output columns of one expert and all its tokens, per pair.
 template <class E, bool FP8, int MF, int NF>
-__global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs p) {
-  __shared__ __attribute__((aligned(16))) float part[4][NF * MF][256];
+__global__ void __launch_bounds__(64 * waves_of(MF)) moe_down_kernel(MoeArgs p) {
+  constexpr int W = waves_of(MF);
+  __shared__ __attribute__((aligned(16))) float part[W / 2][NF * MF][256];
   __shared__ int pair[kMaxTokens];
   const Rows rows = rows_from_ids(p, blockIdx.y, pair);
   if (rows.count == 0) return;
@@ -592,16 +606,15 @@ __global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs p) {
     }
   };
   const int full = I / kBlockK;
-  for (int kb = full * wave / 8; kb < full * (wave + 1) / 8; ++kb) block(kb);
-  if (full < kbs && wave == 7) block(full, typename B::Tail(full * kBlockK, I, g));
+  for (int kb = full * wave / W; kb < full * (wave + 1) / W; ++kb) block(kb);
+  if (full < kbs && wave == W - 1) block(full, typename B::Tail(full * kBlockK, I, g));
   join(total, part, wave, lane);
-  for (int v = threadIdx.x; v < NF * MF * 256; v += 512) {
+  for (int v = threadIdx.x; v < NF * MF * 256; v += 64 * W) {
     const int f = v / 256, at = v % 256;
     const int token = 16 * (f % MF) + (at / 4) % 16;
     const int col = n0 + 16 * (f / MF) + 4 * (at / 64) + at % 4;
     if (token >= rows.count || col >= D) continue;
-    p.part[(int64_t)pair[token] * D + col] =
-        (part[0][f][at] + part[1][f][at]) + (part[2][f][at] + part[3][f][at]);
+    p.part[(int64_t)pair[token] * D + col] = joined(part, f, at);
   }
 }
 
@@ -696,7 +709,7 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
   if (threadIdx.x < 16 && n0 + (int)threadIdx.x < D) {
     const int at = 64 * (threadIdx.x / 4) + threadIdx.x % 4;   // (column 0 of the result: the token)
     p.Y[n0 + threadIdx.x] =
-        E::bits((part[0][0][at] + part[1][0][at]) + (part[2][0][at] + part[3][0][at]));
+        E::bits(joined(part, 0, at));
   }
 }
 
@@ -728,16 +741,16 @@ hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s)
   const int up = row_tiles(a.d_ff, rows, gated ? 2 : 4, cus);
   if (gated) {
     if (up == 2)
-      moe_up_kernel<E, FP8, true, MF, 2><<<grid(a.d_ff, 2, first_rows), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, true, MF, 2><<<grid(a.d_ff, 2, first_rows), 64 * waves_of(MF), 0, s>>>(a);
     else
-      moe_up_kernel<E, FP8, true, MF, 1><<<grid(a.d_ff, 1, first_rows), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, true, MF, 1><<<grid(a.d_ff, 1, first_rows), 64 * waves_of(MF), 0, s>>>(a);
   } else {
     if (up == 4)
-      moe_up_kernel<E, FP8, false, MF, 4><<<grid(a.d_ff, 4, first_rows), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, false, MF, 4><<<grid(a.d_ff, 4, first_rows), 64 * waves_of(MF), 0, s>>>(a);
     else if (up == 2)
-      moe_up_kernel<E, FP8, false, MF, 2><<<grid(a.d_ff, 2, first_rows), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, false, MF, 2><<<grid(a.d_ff, 2, first_rows), 64 * waves_of(MF), 0, s>>>(a);
     else
-      moe_up_kernel<E, FP8, false, MF, 1><<<grid(a.d_ff, 1, first_rows), 512, 0, s>>>(a);
+      moe_up_kernel<E, FP8, false, MF, 1><<<grid(a.d_ff, 1, first_rows), 64 * waves_of(MF), 0, s>>>(a);
   }
   if (a.tokens == 1) {
     moe_down_token_kernel<E, FP8><<<grid(a.d_model, 1, 1), 512, 0, s>>>(a);
@@ -745,11 +758,11 @@ hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s)
   }
   const int down = row_tiles(a.d_model, rows, 4, cus);
   if (down == 4)
-    moe_down_kernel<E, FP8, MF, 4><<<grid(a.d_model, 4, up_rows), 512, 0, s>>>(a);
+    moe_down_kernel<E, FP8, MF, 4><<<grid(a.d_model, 4, up_rows), 64 * waves_of(MF), 0, s>>>(a);
   else if (down == 2)
-    moe_down_kernel<E, FP8, MF, 2><<<grid(a.d_model, 2, up_rows), 512, 0, s>>>(a);
+    moe_down_kernel<E, FP8, MF, 2><<<grid(a.d_model, 2, up_rows), 64 * waves_of(MF), 0, s>>>(a);
   else
-    moe_down_kernel<E, FP8, MF, 1><<<grid(a.d_model, 1, up_rows), 512, 0, s>>>(a);
+    moe_down_kernel<E, FP8, MF, 1><<<grid(a.d_model, 1, up_rows), 64 * waves_of(MF), 0, s>>>(a);
   const unsigned blocks = (unsigned)(((int64_t)a.d_model + 255) / 256);
   moe_combine_kernel<E><<<dim3(blocks, a.tokens), 256, 0, s>>>(a);
   return hipGetLastError();
