@@ -28,6 +28,8 @@
 // rounded to one such number they would cost as much accuracy as the final
 // rounding of Y, and the second MFMA is free beside the loads.  In binary16 hi
 // is clamped to +-65504, the type's range.
+#include <type_traits>
+
 #include "lm_common.h"
 #include "lm_launch.h"
 
@@ -243,9 +245,19 @@ __device__ __forceinline__ Rows rows_from_ids(const MoeArgs& p, int grid_row, in
   return out;
 }
 
-// How a lane reads a block of 128 columns: in chunks of 16 bytes of a weight's
-// row (8 or 16 columns), chunk u of lane group g at column chunk(u, g), as the
-// first operands of four MFMAs; MFMA t multiplies eight columns of chunk t / PER.
+// A value of an input array that is the same for the whole wave, through the
+// scalar cache (a vector load for each scale took as many load instructions as the weights).
+__device__ __forceinline__ float uniform_value(const float* p) {
+  const uint64_t x = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return *reinterpret_cast<const __attribute__((address_space(4))) float*>(lo | (uint64_t)hi << 32);
+}
+
+// How a lane reads a block of K columns of 16 rows (128 bytes of each): in two
+// chunks of 16 bytes of a weight's row (8 or 16 columns), chunk u of lane group g
+// at column chunk(u, g), as the first operands of T MFMAs; MFMA t multiplies eight
+// columns of chunk t / PER.
 //
 // The last, shorter block of a row (Tail): a chunk that crosses the row's end is
 // moved back to the row's last columns, and `mask` keeps those of them that no
@@ -253,19 +265,19 @@ __device__ __forceinline__ Rows rows_from_ids(const MoeArgs& p, int grid_row, in
 // meet a zero).  Rows shorter than a chunk are gathered by element.
 template <class E, bool FP8>
 struct Block {
-  static constexpr int COLS = FP8 ? 16 : 8, CHUNKS = FP8 ? 2 : 4, PER = 4 / CHUNKS;
+  static constexpr int K = FP8 ? 128 : 64, COLS = FP8 ? 16 : 8, T = K / 32, PER = T / 2;
   typedef typename E::vec8 vec8;
-  static __device__ __forceinline__ int chunk(int u, int g) { return FP8 ? 64 * u + 16 * g : 32 * u + 8 * g; }
+  static __device__ __forceinline__ int chunk(int u, int g) { return K / 2 * u + COLS * g; }
 
   struct Tail {
-    int at[CHUNKS];        // first column
-    u32x4 mask[4];         // of the eight columns of MFMA t, 16 bits each
-    u32x4 mask8[CHUNKS];   // e4m3: of the chunk's 16 bytes
-    int tiny;              // the row's columns, if fewer than a chunk (else 0)
+    int at[2];        // first column
+    u32x4 mask[T];    // of the eight columns of MFMA t, 16 bits each
+    u32x4 mask8[2];   // e4m3: of the chunk's 16 bytes
+    int tiny;         // the row's columns, if fewer than a chunk (else 0)
     __device__ __forceinline__ Tail(int k0, int cols, int g) {
       tiny = cols < COLS ? cols : 0;
 #pragma unroll
-      for (int u = 0; u < CHUNKS; ++u) {
+      for (int u = 0; u < 2; ++u) {
         const int first = k0 + chunk(u, g);
         at[u] = tiny ? 0 : first < cols - COLS ? first : cols - COLS;
         // Columns at[u] + c count if they are not before `first` (nor past the end).
@@ -290,25 +302,23 @@ struct Block {
     }
   };
 
-  vec8 v[4];
-  __device__ __forceinline__ void set(int u, u32x4 c) {
-    if constexpr (FP8) {
-      v[2 * u] = E::widen(c[0], c[1]);
-      v[2 * u + 1] = E::widen(c[2], c[3]);
-    } else {
-      v[u] = __builtin_bit_cast(vec8, c);
-    }
+  u32x4 c[2];   // as loaded (widened only when it is multiplied: a block on its way takes 8 registers)
+  __device__ __forceinline__ vec8 operand(int t) const {
+    if constexpr (FP8)
+      return t % 2 ? E::widen(c[t / 2][2], c[t / 2][3]) : E::widen(c[t / 2][0], c[t / 2][1]);
+    else
+      return __builtin_bit_cast(vec8, c[t]);
   }
   __device__ __forceinline__ void load(const uint8_t* row, int k0, int g) {
 #pragma unroll
-    for (int u = 0; u < CHUNKS; ++u) set(u, load16(row + (k0 + chunk(u, g)) * (FP8 ? 1 : 2)));
+    for (int u = 0; u < 2; ++u) c[u] = load16(row + (k0 + chunk(u, g)) * (FP8 ? 1 : 2));
   }
   __device__ __forceinline__ void load(const uint8_t* row, const Tail& tail) {
 #pragma unroll
-    for (int u = 0; u < CHUNKS; ++u) {
-      const u32x4 c = tail.tiny ? gather(row, tail.tiny * (FP8 ? 1 : 2))
+    for (int u = 0; u < 2; ++u) {
+      const u32x4 x = tail.tiny ? gather(row, tail.tiny * (FP8 ? 1 : 2))
                                 : load16(row + tail.at[u] * (FP8 ? 1 : 2));
-      set(u, c & (FP8 ? tail.mask8[u] : tail.mask[u]));
+      c[u] = x & (FP8 ? tail.mask8[u] : tail.mask[u * PER]);
     }
   }
   static __device__ __forceinline__ vec8 tokens(const uint16_t* row, int k0, int g, int t) {
@@ -316,9 +326,9 @@ struct Block {
   }
   static __device__ __forceinline__ vec8 tokens(const uint16_t* row, const Tail& tail, int t) {
     const int at = tail.at[t / PER] + 8 * (t % PER);
-    const u32x4 c = tail.tiny ? gather(reinterpret_cast<const uint8_t*>(row + at), 2 * (tail.tiny - at))
+    const u32x4 x = tail.tiny ? gather(reinterpret_cast<const uint8_t*>(row + at), 2 * (tail.tiny - at))
                               : load16(row + at);
-    return __builtin_bit_cast(vec8, c & tail.mask[t]);
+    return __builtin_bit_cast(vec8, x & tail.mask[t]);
   }
   // The first `bytes` (fewer than 32) bytes of a row, up to 16.
   static __device__ __forceinline__ u32x4 gather(const uint8_t* row, int bytes) {
@@ -400,9 +410,55 @@ __device__ __forceinline__ float joined(const float (&part)[H][F][256], int f, i
 // two on a compute unit, one starting or ending while the other reads.
 constexpr int waves_of(int mf) { return mf == 4 ? 4 : 8; }
 
+// A wave's whole blocks first .. end - 1 of F weight rows' fragments: the next
+// block of weights is on its way while this one is multiplied.  The tokens of a
+// block are asked for before the next weights (loads return in order), all at
+// once where they fit the registers.  `load_weights(B (&)[F], kb)`,
+// `load_tokens(X&, i, kb)`, `multiply(B (&)[F], X&, i, kb)`; `count` tokens of at
+// most 16 MF.  AHEAD false: without the block ahead, which pays with 16-bit
+// weights (64 tokens, 8 experts: 405 -> 344 and 234 -> 198 us); e4m3 blocks hold twice
+// the columns, and the registers are worth more as occupancy (4 tokens, 64
+// experts: 73 and 49 us without, 100 and 65 with).
+template <int MF, int F, int ALL, bool AHEAD, class B, class X, class LW, class LT, class M>
+__device__ __forceinline__ void stream_blocks(int first, int end, int count, LW load_weights,
+                                              LT load_tokens, M multiply) {
+  if (first >= end) return;
+  auto run = [&](auto active) __attribute__((always_inline)) {
+    constexpr int MA = decltype(active)::value, HELD = MA < ALL ? MA : ALL;
+    B weights[AHEAD ? 2 : 1][F];
+    if constexpr (AHEAD) load_weights(weights[0], first);
+    for (int kb = first; kb < end; kb += 2) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = kb + u;
+        if (at >= end) break;
+        X tokens[HELD];
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) load_tokens(tokens[i], i, at);
+        if constexpr (AHEAD)
+          load_weights(weights[1 - u], at + 1 < end ? at + 1 : at);
+        else
+          load_weights(weights[0], at);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MA; ++i) {
+          if (i >= HELD) load_tokens(tokens[i % HELD], i, at);
+          multiply(weights[AHEAD ? u : 0], tokens[i % HELD], i, at);
+        }
+      }
+    }
+  };
+  if (count <= 16 || MF == 1)
+    run(std::integral_constant<int, 1>());
+  else if (count <= 32 || MF == 2)
+    run(std::integral_constant<int, MF < 2 ? MF : 2>());
+  else
+    run(std::integral_constant<int, MF>());
+}
+
 // h for 16 NF inner columns of one expert and all its tokens (at most 16 MF).
 template <class E, bool FP8, bool GATED, int MF, int NF>
-__global__ void __launch_bounds__(64 * waves_of(MF)) moe_up_kernel(MoeArgs p) {
+__global__ void __launch_bounds__(64 * waves_of(MF)) __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_up_kernel(MoeArgs p) {
   constexpr int SIDES = GATED ? 2 : 1, W = waves_of(MF);
   __shared__ __attribute__((aligned(16))) float part[W / 2][SIDES * NF * MF][256];
   __shared__ int pair[kMaxTokens], slots[kMaxTokens], found;
@@ -460,52 +516,65 @@ __global__ void __launch_bounds__(64 * waves_of(MF)) moe_up_kernel(MoeArgs p) {
 #pragma unroll
   for (int f = 0; f < SIDES * NF * MF; ++f) total[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   typedef Block<E, FP8> B;
-  auto block = [&](int kb, auto... tail) __attribute__((always_inline)) {
-    B wb[SIDES][NF];
+  constexpr int F = SIDES * NF;
+  struct X {
+    typename E::vec8 v[B::T];
+    float s0[FP8 ? F : 1], s1[FP8 ? F : 1];   // scales of the block (with the first 16 tokens)
+  };
+  auto load_scales = [&](X& t, int kb) __attribute__((always_inline)) {
+    if constexpr (FP8) {
 #pragma unroll
-    for (int side = 0; side < SIDES; ++side)
-#pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        if constexpr (sizeof...(tail) > 0)
-          wb[side][j].load(w[side][j], tail...);
-        else
-          wb[side][j].load(w[side][j], kb * kBlockK, g);
+      for (int f = 0; f < F; ++f) {
+        const float* s = scale[f / NF][f % NF] + kb * rbs;
+        t.s0[f] = uniform_value(s);
+        t.s1[f] = uniform_value(s + (edge[f / NF][f % NF] < 16 ? 1 : 0));
       }
+    }
+  };
+  auto multiply = [&](B (&wb)[F], X& t, int i, int) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      f32x4& sum = total[f * MF + i];
+      f32x4 v = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum;
+#pragma unroll
+      for (int m = 0; m < B::T; ++m) v = E::mfma(wb[f].operand(m), t.v[m], v);
+      if constexpr (FP8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sum[e] = __builtin_fmaf(v[e], 4 * g + e < edge[f / NF][f % NF] ? t.s0[f] : t.s1[f], sum[e]);
+      } else {
+        sum = v;
+      }
+    }
+  };
+  const int full = D / B::K;
+  stream_blocks<MF, F, FP8 ? 1 : 4, !FP8, B, X>(
+      full * wave / W, full * (wave + 1) / W, count,
+      [&](B (&wb)[F], int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) wb[f].load(w[f / NF][f % NF], kb * B::K, g);
+      },
+      [&](X& t, int i, int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < B::T; ++m) t.v[m] = B::tokens(x[i], kb * B::K, g, m);
+        load_scales(t, kb);
+      },
+      multiply);
+  if (full * B::K < D && wave == W - 1) {
+    const typename B::Tail tail(full * B::K, D, g);
+    B wb[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) wb[f].load(w[f / NF][f % NF], tail);
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       if (16 * i >= count) break;
-      typename E::vec8 xv[4];
+      X t;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if constexpr (sizeof...(tail) > 0)
-          xv[t] = B::tokens(x[i], tail..., t);
-        else
-          xv[t] = B::tokens(x[i], kb * kBlockK, g, t);
-      }
-#pragma unroll
-      for (int side = 0; side < SIDES; ++side)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-          f32x4& sum = total[(side * NF + j) * MF + i];
-          if constexpr (FP8) {
-            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) v = E::mfma(wb[side][j].v[t], xv[t], v);
-            const float* s = scale[side][j] + kb * rbs;
-            const float s0 = s[0], s1 = edge[side][j] < 16 ? s[1] : 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sum[e] = __builtin_fmaf(v[e], 4 * g + e < edge[side][j] ? s0 : s1, sum[e]);
-          } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) sum = E::mfma(wb[side][j].v[t], xv[t], sum);
-          }
-        }
+      for (int m = 0; m < B::T; ++m) t.v[m] = B::tokens(x[i], tail, m);
+      load_scales(t, full);
+      multiply(wb, t, i, full);
     }
-  };
-  const int full = D / kBlockK;
-  for (int kb = full * wave / W; kb < full * (wave + 1) / W; ++kb) block(kb);
-  if (full < kbs && wave == W - 1) block(full, typename B::Tail(full * kBlockK, D, g));
+  }
   join(total, part, wave, lane);
   for (int v = threadIdx.x; v < NF * MF * 256; v += 64 * W) {
     const int f = v / 256, at = v % 256;
@@ -531,7 +600,7 @@ __global__ void __launch_bounds__(64 * waves_of(MF)) moe_up_kernel(MoeArgs p) {
 
 // h W2 of 16 NF output columns of one expert and all its tokens, per pair.
 template <class E, bool FP8, int MF, int NF>
-__global__ void __launch_bounds__(64 * waves_of(MF)) moe_down_kernel(MoeArgs p) {
+__global__ void __launch_bounds__(64 * waves_of(MF)) __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_down_kernel(MoeArgs p) {
   constexpr int W = waves_of(MF);
   __shared__ __attribute__((aligned(16))) float part[W / 2][NF * MF][256];
   __shared__ int pair[kMaxTokens];
@@ -563,51 +632,63 @@ __global__ void __launch_bounds__(64 * waves_of(MF)) moe_down_kernel(MoeArgs p) 
 #pragma unroll
   for (int f = 0; f < NF * MF; ++f) total[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   typedef Block<E, FP8> B;
-  auto block = [&](int kb, auto... tail) __attribute__((always_inline)) {
-    B wb[NF];
+  struct X {
+    typename E::vec8 hi[B::T], lo[B::T];
+    float scale;
+  };
+  auto multiply = [&](B (&wb)[NF], X& t, int i, int) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      if constexpr (sizeof...(tail) > 0)
-        wb[j].load(w[j], tail...);
-      else
-        wb[j].load(w[j], kb * kBlockK, g);
-    }
-    const float s = FP8 ? scale[kb * rbs] : 1.0f;
+      f32x4& sum = total[j * MF + i];
+      f32x4 v = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum;
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      if (16 * i >= rows.count) break;
-      typename E::vec8 hi[4], lo[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if constexpr (sizeof...(tail) > 0) {
-          hi[t] = B::tokens(p.h_hi + h_row[i], tail..., t);
-          lo[t] = B::tokens(p.h_lo + h_row[i], tail..., t);
-        } else {
-          hi[t] = B::tokens(p.h_hi + h_row[i], kb * kBlockK, g, t);
-          lo[t] = B::tokens(p.h_lo + h_row[i], kb * kBlockK, g, t);
-        }
+      for (int m = 0; m < B::T; ++m) {
+        const typename E::vec8 a = wb[j].operand(m);
+        v = E::mfma(a, t.lo[m], v);
+        v = E::mfma(a, t.hi[m], v);
       }
+      if constexpr (FP8) {
 #pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        f32x4& sum = total[j * MF + i];
-        f32x4 v = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          v = E::mfma(wb[j].v[t], lo[t], v);
-          v = E::mfma(wb[j].v[t], hi[t], v);
-        }
-        if constexpr (FP8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(v[e], s, sum[e]);
-        } else {
-          sum = v;
-        }
+        for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(v[e], t.scale, sum[e]);
+      } else {
+        sum = v;
       }
     }
   };
-  const int full = I / kBlockK;
-  for (int kb = full * wave / W; kb < full * (wave + 1) / W; ++kb) block(kb);
-  if (full < kbs && wave == W - 1) block(full, typename B::Tail(full * kBlockK, I, g));
+  const int full = I / B::K;
+  stream_blocks<MF, NF, FP8 ? 1 : 2, !FP8, B, X>(
+      full * wave / W, full * (wave + 1) / W, rows.count,
+      [&](B (&wb)[NF], int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) wb[j].load(w[j], kb * B::K, g);
+      },
+      [&](X& t, int i, int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < B::T; ++m) {
+          t.hi[m] = B::tokens(p.h_hi + h_row[i], kb * B::K, g, m);
+          t.lo[m] = B::tokens(p.h_lo + h_row[i], kb * B::K, g, m);
+        }
+        t.scale = FP8 ? uniform_value(scale + kb * rbs) : 1.0f;
+      },
+      multiply);
+  if (full * B::K < I && wave == W - 1) {
+    const typename B::Tail tail(full * B::K, I, g);
+    B wb[NF];
+#pragma unroll
+    for (int j = 0; j < NF; ++j) wb[j].load(w[j], tail);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      if (16 * i >= rows.count) break;
+      X t;
+#pragma unroll
+      for (int m = 0; m < B::T; ++m) {
+        t.hi[m] = B::tokens(p.h_hi + h_row[i], tail, m);
+        t.lo[m] = B::tokens(p.h_lo + h_row[i], tail, m);
+      }
+      t.scale = FP8 ? uniform_value(scale + full * rbs) : 1.0f;
+      multiply(wb, t, i, full);
+    }
+  }
   join(total, part, wave, lane);
   for (int v = threadIdx.x; v < NF * MF * 256; v += 64 * W) {
     const int f = v / 256, at = v % 256;
@@ -632,7 +713,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs p) {
 }
 
 // One token: 16 columns of Y per workgroup from all its experts.  The units of
-// work are (slot, 128 columns), wave w taking an eighth of them.  The order of the
+// work are (slot, block of columns), wave w taking an eighth of them.  The order of the
 // sum is fixed by the shape.
 template <class E, bool FP8>
 __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
@@ -645,7 +726,7 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
   const int D = p.d_model, I = p.d_ff;
   const int n = n0 + r < D ? n0 + r : D - 1;
   const int64_t rbs = (D + 127) / 128;
-  const int kbs = (I + 127) / 128, full = I / kBlockK;
+  const int kbs = (I + 127) / 128, full = I / B::K;
   const int mine = p.ids[lane < p.top_k ? lane : 0];
   const float weight = p.w[lane < p.top_k ? lane : 0];
   f32x4 total[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
@@ -661,20 +742,20 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) total[0][e] = __builtin_fmaf(v[e], f, total[0][e]);
   };
-  constexpr int AHEAD = 2;   // units whose loads are in flight together
+  constexpr int AHEAD = FP8 ? 2 : 4;   // units whose loads are in flight together
   const int units = p.top_k * full, end = units * (wave + 1) / 8;
   for (int u0 = units * wave / 8; u0 < end; u0 += AHEAD) {
     B wb[AHEAD];
-    typename E::vec8 hi[AHEAD][4], lo[AHEAD][4];
+    typename E::vec8 hi[AHEAD][B::T], lo[AHEAD][B::T];
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
       const int u = u0 + a < end ? u0 + a : end - 1;
       const int s = u / full, kb = u % full;
-      wb[a].load(row(s), kb * kBlockK, g);
+      wb[a].load(row(s), kb * B::K, g);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        hi[a][t] = B::tokens(p.h_hi + s * p.ldh, kb * kBlockK, g, t);
-        lo[a][t] = B::tokens(p.h_lo + s * p.ldh, kb * kBlockK, g, t);
+      for (int t = 0; t < B::T; ++t) {
+        hi[a][t] = B::tokens(p.h_hi + s * p.ldh, kb * B::K, g, t);
+        lo[a][t] = B::tokens(p.h_lo + s * p.ldh, kb * B::K, g, t);
       }
     }
     __builtin_amdgcn_sched_barrier(0);   // (all issued before anything waits)
@@ -683,24 +764,24 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
       if (u0 + a >= end) break;
       f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        v = E::mfma(wb[a].v[t], lo[a][t], v);
-        v = E::mfma(wb[a].v[t], hi[a][t], v);
+      for (int t = 0; t < B::T; ++t) {
+        v = E::mfma(wb[a].operand(t), lo[a][t], v);
+        v = E::mfma(wb[a].operand(t), hi[a][t], v);
       }
       add(v, (u0 + a) / full, (u0 + a) % full);
     }
   }
-  if (full < kbs) {
-    const typename B::Tail tail(full * kBlockK, I, g);
+  if (full * B::K < I) {
+    const typename B::Tail tail(full * B::K, I, g);
 #pragma unroll 1
     for (int s = wave; s < p.top_k; s += 8) {
       B wb;
       wb.load(row(s), tail);
       f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        v = E::mfma(wb.v[t], B::tokens(p.h_lo + s * p.ldh, tail, t), v);
-        v = E::mfma(wb.v[t], B::tokens(p.h_hi + s * p.ldh, tail, t), v);
+      for (int t = 0; t < B::T; ++t) {
+        v = E::mfma(wb.operand(t), B::tokens(p.h_lo + s * p.ldh, tail, t), v);
+        v = E::mfma(wb.operand(t), B::tokens(p.h_hi + s * p.ldh, tail, t), v);
       }
       add(v, s, full);
     }
@@ -738,20 +819,25 @@ hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s)
   const auto grid = [](int n, int nf, int y) {
     return dim3((unsigned)(((int64_t)n + 16 * nf - 1) / (16 * nf)), y);
   };
-  const int up = row_tiles(a.d_ff, rows, gated ? 2 : 4, cus);
-  if (gated) {
-    if (up == 2)
-      moe_up_kernel<E, FP8, true, MF, 2><<<grid(a.d_ff, 2, first_rows), 64 * waves_of(MF), 0, s>>>(a);
-    else
-      moe_up_kernel<E, FP8, true, MF, 1><<<grid(a.d_ff, 1, first_rows), 64 * waves_of(MF), 0, s>>>(a);
-  } else {
-    if (up == 4)
-      moe_up_kernel<E, FP8, false, MF, 4><<<grid(a.d_ff, 4, first_rows), 64 * waves_of(MF), 0, s>>>(a);
-    else if (up == 2)
-      moe_up_kernel<E, FP8, false, MF, 2><<<grid(a.d_ff, 2, first_rows), 64 * waves_of(MF), 0, s>>>(a);
-    else
-      moe_up_kernel<E, FP8, false, MF, 1><<<grid(a.d_ff, 1, first_rows), 64 * waves_of(MF), 0, s>>>(a);
-  }
+  // (With e4m3 weights and 64 tokens the widest tile does not fit the registers.)
+  constexpr int WIDE = FP8 && MF == 4 ? 2 : 4;
+  const int up = row_tiles(a.d_ff, rows, gated ? WIDE / 2 : WIDE, cus);
+  const auto launch_up = [&](auto is_gated, auto nf) {
+    constexpr int NF = decltype(nf)::value;
+    moe_up_kernel<E, FP8, decltype(is_gated)::value, MF, NF>
+        <<<grid(a.d_ff, NF, first_rows), 64 * waves_of(MF), 0, s>>>(a);
+  };
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, WIDE> wide{};
+  constexpr std::integral_constant<int, WIDE / 2> half{};
+  if (gated)
+    up == WIDE / 2 ? launch_up(std::true_type(), half) : launch_up(std::true_type(), one);
+  else
+    up == WIDE ? launch_up(std::false_type(), wide)
+    : up == 2  ? launch_up(std::false_type(), two)
+               : launch_up(std::false_type(), one);
+  // (One token: 16 columns of Y from all its experts per workgroup.)
   if (a.tokens == 1) {
     moe_down_token_kernel<E, FP8><<<grid(a.d_model, 1, 1), 512, 0, s>>>(a);
     return hipGetLastError();
