@@ -125,7 +125,10 @@ __global__ void __launch_bounds__(512) fp8_ksplit_kernel(Fp8Call p) {
 #pragma unroll
         for (int j = 0; j < (ROWB ? NF : 1); ++j)
 #pragma unroll
-          for (int e = 0; e < (ROWB ? 4 : 1); ++e) s.b[j][e] = sb[j][e][(int64_t)kb * p.ldsb];
+          for (int e = 0; e < (ROWB ? 4 : 1); ++e) {
+            const float* at = sb[j][e] + (int64_t)kb * p.ldsb;
+            s.b[j][e] = ROWB ? *at : uniform_value(at);
+          }
       };
       auto add = [&](const Frag& a, const Frag& b, const Scales& s, int i, int j)
           __attribute__((always_inline)) {
@@ -269,7 +272,7 @@ int fp8_tile(const Fp8Call& c, int cus, int force) {
     return (((int64_t)c.M + m - 1) / m) * (((int64_t)c.N + n - 1) / n);
   };
   // 32-bit row and tile numbers in the tiled kernels.
-  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) && tiles(64, 64) < (1 << 24);
+  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) && tiles(64, 64) < (1 << 23);   // (fewer than 2^32 threads)
   const bool direct = fp8_direct(c), wide = c.fast_sums && c.b_rows == 128;
   static const int kSplit[6][2] = {{64, 32}, {64, 16}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
   int tile = force;

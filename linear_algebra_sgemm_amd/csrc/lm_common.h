@@ -17,8 +17,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 // The same vectors at any byte address: gfx950 serves global loads and stores
-// of up to 16 bytes at any alignment (at full speed within a 16-byte line), so
-// rows of any length take the same code path.
+// of up to 16 bytes at any alignment, so rows of any length take the same code path.
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
@@ -70,6 +69,15 @@ __device__ __forceinline__ u32x4 load8h_upto(const uint16_t* p, int valid) {
   for (int e = 0; e < 8; ++e)
     if (e < valid) v[e / 2] |= (uint32_t)p[e] << (16 * (e % 2));
   return v;
+}
+
+// A value of an input array that is the same for the whole wave, through the
+// scalar cache (a vector load for each scale took as many load instructions as the weights).
+__device__ __forceinline__ float uniform_value(const float* p) {
+  const uint64_t x = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return *reinterpret_cast<const __attribute__((address_space(4))) float*>(lo | (uint64_t)hi << 32);
 }
 
 // Eight e4m3 bytes as eight 16-bit values.  Exact: e4m3's 4 significant bits

@@ -245,15 +245,6 @@ __device__ __forceinline__ Rows rows_from_ids(const MoeArgs& p, int grid_row, in
   return out;
 }
 
-// A value of an input array that is the same for the whole wave, through the
-// scalar cache (a vector load for each scale took as many load instructions as the weights).
-__device__ __forceinline__ float uniform_value(const float* p) {
-  const uint64_t x = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
-  return *reinterpret_cast<const __attribute__((address_space(4))) float*>(lo | (uint64_t)hi << 32);
-}
-
 // How a lane reads a block of K columns of 16 rows (128 bytes of each): in two
 // chunks of 16 bytes of a weight's row (8 or 16 columns), chunk u of lane group g
 // at column chunk(u, g), as the first operands of T MFMAs; MFMA t multiplies eight
