@@ -38,9 +38,10 @@ extern "C" {
  * eight waves split K between them (any operands; small outputs; never split
  * across workgroups).  op 2 = fp8_gemm_bias_act: 0 = 128 x 256 tiles (fast
  * sums with one scale per 128 rows of B, else 1), 1 = 128 x 128 and 2 = 64 x 64
- * tiles copied straight into LDS (else 3), 3 = 128 x 128 tiles through registers,
- * and tiles whose eight waves split K between them: 4 = 64 x 32, 5 = 64 x 16, 6 = 32
- * x 32, 7 = 32 x 16, 8 = 16 x 32, 9 = 16 x 16.
+ * tiles copied straight into LDS, 3 = tile 2 with three stages instead of four
+ * (all four else 4), 4 = 128 x 128 tiles through registers, and tiles whose eight
+ * waves split K between them: 5 = 64 x 32 (with one scale per row of B and FP32
+ * sums 6), 6 = 64 x 16, 7 = 32 x 32, 8 = 32 x 16, 9 = 16 x 32, 10 = 16 x 16.
  * Whether the aligned fast path or the
  * bounds-checked path runs still follows the shape and alignment.  Returns
  * GEMM_STATUS_INVALID_VALUE for an unknown op or tile.  Pure host state: no

@@ -34,8 +34,8 @@ __device__ __forceinline__ void store_c(const Fp8Call& p, int64_t row, int64_t c
   }
 }
 
-// The tiled kernels (fp8_tile_kernels.hip): tiles 0 to 3 of fp8_tile.  Tiles 0
-// to 2 copy straight into LDS, which the call has to allow (fp8_direct).
+// The tiled kernels (fp8_tile_kernels.hip): tiles 0 to 4 of fp8_tile.  Tiles 0
+// to 3 copy straight into LDS, which the call has to allow (fp8_direct).
 bool fp8_direct(const Fp8Call& c);
 hipError_t launch_fp8_tile(const Fp8Call& c, int tile, hipStream_t s);
 

@@ -264,9 +264,11 @@ hipError_t launch_ksplit(const Fp8Call& c, hipStream_t s) {
 //  * K-split tiles of m x n take (m + n) K bytes through a CU's load path at 23
 //    bytes a nanosecond.
 // So 24 x 4096 x 4096 runs 32 x 16 K-split tiles (9.4 us; 64 x 64: 15.5), 64 x
-// 14336 x 4096 the 64 x 64 ones (17; K-split 31), 1000 x 3000 x 777 and up to a few
-// tiles per CU 64 x 64 or 128 x 128 (the same there), 4096 x 14336 x 4096 128 x 256 (230;
-// 128 x 128: 245).  Through registers a tile takes about twice its time.
+// 14336 x 4096 the 64 x 64 ones (13; K-split 31), 4096 x 14336 x 4096 128 x 256 (230;
+// 128 x 128: 245).  Through registers a tile takes about twice its time.  Of the 64 x
+// 64 tiles the one with three stages lets three workgroups share a CU, which
+// pays where all run at once that way and not with two (1000 x 3000 x 777, 752 tiles:
+// 10.9 against 12.8; 512 x 4096 x 4096, 512 tiles: 18.3 against 17.3).
 int fp8_tile(const Fp8Call& c, int cus, int force) {
   const auto tiles = [&](int m, int n) {
     return (((int64_t)c.M + m - 1) / m) * (((int64_t)c.N + n - 1) / n);
@@ -296,33 +298,33 @@ int fp8_tile(const Fp8Call& c, int cus, int force) {
       if (direct) {
         if (wide) offer(0, ring(128, 256, 1250, 1800));
         offer(1, t128);
-        offer(2, t64);
+        offer(tiles(64, 64) > 2 * cus && tiles(64, 64) <= 3 * cus ? 3 : 2, t64);
       } else {
-        offer(3, 2 * t128);
+        offer(4, 2 * t128);
       }
     }
     for (int i = !c.fast_sums && c.b_rows == 1; i < 6; ++i) {
       const int m = kSplit[i][0], n = kSplit[i][1];
       const double rounds = (double)((tiles(m, n) + cus - 1) / cus);
-      offer(4 + i, rounds * (m + n) * ((double)c.K + 512) / 23);
+      offer(5 + i, rounds * (m + n) * ((double)c.K + 512) / 23);
     }
   }
-  if (tile < 4 && !tiled) tile = 4;
-  if (tile < 3 && !direct) tile = 3;
+  if (tile < 5 && !tiled) tile = 5;
+  if (tile < 4 && !direct) tile = 4;
   if (tile == 0 && !wide) tile = 1;
-  if (tile == 4 && !c.fast_sums && c.b_rows == 1) tile = 5;
+  if (tile == 5 && !c.fast_sums && c.b_rows == 1) tile = 6;
   return tile;
 }
 
 hipError_t launch_fp8_gemm(const Fp8Call& c, int cus, int force, hipStream_t s) {
   const int tile = fp8_tile(c, cus, force);
   switch (tile) {
-    case 4: return launch_ksplit<4, 2>(c, s);
-    case 5: return launch_ksplit<4, 1>(c, s);
-    case 6: return launch_ksplit<2, 2>(c, s);
-    case 7: return launch_ksplit<2, 1>(c, s);
-    case 8: return launch_ksplit<1, 2>(c, s);
-    case 9: return launch_ksplit<1, 1>(c, s);
+    case 5: return launch_ksplit<4, 2>(c, s);
+    case 6: return launch_ksplit<4, 1>(c, s);
+    case 7: return launch_ksplit<2, 2>(c, s);
+    case 8: return launch_ksplit<2, 1>(c, s);
+    case 9: return launch_ksplit<1, 2>(c, s);
+    case 10: return launch_ksplit<1, 1>(c, s);
     default: return launch_fp8_tile(c, tile, s);
   }
 }

@@ -209,7 +209,7 @@ __device__ __forceinline__ void write_back(const Fp8Call& c, const f32x16 (&tota
 }  // namespace
 
 template <class T>
-__global__ void __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ void __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(2)))
 fp8_tile_kernel(Fp8TileArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS_BYTES];
   const Fp8Call& c = p.c;
@@ -454,6 +454,7 @@ hipError_t launch_fp8_tile(const Fp8Call& c, int tile, hipStream_t s) {
     case 0: return launch_tile<Fp8Tile<128, 256, 1, 4, 2, true, false, true>>(c, s);
     case 1: return launch_as<128, 128, 2, 2, 2, true>(c, s);
     case 2: return launch_as<64, 64, 2, 2, 4, true>(c, s);
+    case 3: return launch_as<64, 64, 2, 2, 3, true>(c, s);   // (three workgroups per CU)
     default: return launch_as<128, 128, 2, 2, 2, false>(c, s);
   }
 }

@@ -55,10 +55,10 @@ struct Fp8Call {
   bool fast_sums;
 };
 // Output tile: 0 = 128 x 256 (fast sums and one scale per 128 rows of B only), 1 =
-// 128 x 128, 2 = 64 x 64, copied straight into LDS; 3 = 128 x 128 for other
-// operands; with K split over a workgroup's waves 4 = 64 x 32, 5 = 64 x 16, 6 = 32
-// x 32, 7 = 32 x 16, 8 = 16 x 32 and 9 = 16 x 16.
-constexpr int kFp8TileCount = 10;
+// 128 x 128, 2 = 64 x 64 with four stages of LDS, 3 = with three, copied straight
+// into LDS; 4 = 128 x 128 for other operands; with K split over a workgroup's
+// waves 5 = 64 x 32, 6 = 64 x 16, 7 = 32 x 32, 8 = 32 x 16, 9 = 16 x 32 and 10 = 16 x 16.
+constexpr int kFp8TileCount = 11;
 // The tile that runs for a call on `cus` compute units: `force`, or by shape
 // where that is -1; resolved to one that applies.
 int fp8_tile(const Fp8Call& c, int cus, int force);

@@ -241,7 +241,7 @@ def test_product(M, N, K, fast):
 
 
 @pytest.mark.parametrize("fast", [False, True])
-@pytest.mark.parametrize("tile", range(10))
+@pytest.mark.parametrize("tile", range(11))
 @pytest.mark.parametrize("M,N,K", [(256, 256, 256), (512, 384, 1152), (257, 513, 640), (70, 40, 384),
                                    (300, 260, 393), (1, 1, 1), (130, 129, 100), (60, 70, 4240)])
 def test_every_tile(M, N, K, tile, fast):

@@ -134,9 +134,9 @@ def test_workspace_size():
 
 
 def test_forced_tiles():
-    for tile in range(-1, 10):
+    for tile in range(-1, 11):
         assert lib.gemm_debug_force_tile(2, tile) == lib.STATUS_SUCCESS
     assert lib.gemm_debug_force_tile(2, -1) == lib.STATUS_SUCCESS
-    assert lib.gemm_debug_force_tile(2, 10) == BAD
+    assert lib.gemm_debug_force_tile(2, 11) == BAD
     assert lib.gemm_debug_force_tile(2, -2) == BAD
     assert lib.gemm_debug_force_tile(3, 0) == BAD
