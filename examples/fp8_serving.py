@@ -40,7 +40,8 @@ class Step:
         def normal(*shape, size=1.0):
             return torch.randn(shape, generator=g, device="cuda") * size
         self.wp, self.bias = normal(1, d, d, size=d ** -0.5), normal(d, size=0.1)
-        self.w1, self.w2 = normal(experts, 2 * i, d, size=d ** -0.5), normal(experts, d, i, size=i ** -0.5)
+        self.w1 = normal(experts, 2 * i, d, size=d ** -0.5)
+        self.w2 = normal(experts, d, i, size=i ** -0.5)
         self.router = normal(experts, d, size=1.5 * d ** -0.5).bfloat16()
         self.x = normal(tokens, d).bfloat16()
         self.qp, self.sp = quantize_weights(self.wp)

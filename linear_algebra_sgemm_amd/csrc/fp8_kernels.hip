@@ -65,6 +65,34 @@ __device__ __forceinline__ f32x4 block_product(const Frag& x, const Frag& y) {
   }
 }
 
+// Four consecutive values of one row of C (columns col ..; `left` of them exist).
+__device__ __forceinline__ void store_c(const Fp8Call& p, int64_t row, int64_t col, f32x4 v) {
+  const int64_t left = p.N - col;
+  if (p.type == GEMM_TYPE_F32) {
+    float* d = static_cast<float*>(p.C) + row * p.ldc + col;
+    if (left >= 4) {
+      *reinterpret_cast<f32x4_any*>(d) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) d[e] = v[e];
+    }
+    return;
+  }
+  uint16_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    h[e] = p.type == GEMM_TYPE_F16 ? LmF16::bits(v[e]) : LmBF16::bits(v[e]);
+  uint16_t* d = static_cast<uint16_t*>(p.C) + row * p.ldc + col;
+  if (left >= 4) {
+    *reinterpret_cast<u32x2_any*>(d) = __builtin_bit_cast(u32x2, h);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) d[e] = h[e];
+  }
+}
+
 }  // namespace
 
 // 16 MF x 16 NF output tile per workgroup, its eight waves taking an eighth of
@@ -274,7 +302,8 @@ int fp8_tile(const Fp8Call& c, int cus, int force) {
     return (((int64_t)c.M + m - 1) / m) * (((int64_t)c.N + n - 1) / n);
   };
   // 32-bit row and tile numbers in the tiled kernels.
-  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) && tiles(64, 64) < (1 << 23);   // (fewer than 2^32 threads)
+  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) &&
+                     tiles(64, 64) < (1 << 23);   // (fewer than 2^32 threads)
   const bool direct = fp8_direct(c), wide = c.fast_sums && c.b_rows == 128;
   static const int kSplit[6][2] = {{64, 32}, {64, 16}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
   int tile = force;
@@ -287,7 +316,8 @@ int fp8_tile(const Fp8Call& c, int cus, int force) {
       }
     };
     if (tiled) {
-      const double blocks = (double)(((int64_t)c.K + kBlockK - 1) / kBlockK) + 2;   // (start and end: two more)
+      // (start and end count as two blocks)
+      const double blocks = (double)(((int64_t)c.K + kBlockK - 1) / kBlockK) + 2;
       const auto ring = [&](int m, int n, double one, double two) {
         const double per_cu = (double)tiles(m, n) / cus;
         return blocks * (per_cu <= 1 ? one : per_cu <= 2 ? two : two * per_cu / 2);

@@ -3,8 +3,8 @@
 // the matrix units bound it.
 //
 // One K tile is one block of 128 columns: rows of 128 bytes, copied from memory
-// straight into LDS (16 bytes a lane, whole 128-byte lines), two tiles in
-// flight.  Row r's eight 16-byte chunks lie permuted by (r / 2) % 8, so that the
+// straight into LDS (16 bytes a lane, whole 128-byte lines) one to three tiles
+// ahead.  Row r's eight 16-byte chunks lie permuted by (r / 2) % 8, so that the
 // fragment reads of 16 neighbouring rows fall into 16 different bank groups.
 // The block's scales travel the same way, 4 bytes a lane.
 //
@@ -13,6 +13,14 @@
 // fp32 totals on the vector unit while the matrix unit works on the next
 // block.  B is the first operand, so a lane holds the columns 8 q + 4 (lane / 32) + 0..3 of
 // one row of C: one scale of A per lane and block, and 4-column stores.
+//
+// What bounds it: the scaling is 16 FMAs (64 cycles) of vector work beside 128
+// cycles of 8-bit MFMAs in a block; with the operands widened, and a scale for
+// every row of B, about 300 beside 256.  Measured: 4096 x 14336 x 4096 with GELU 250
+// us (1920 TFLOP/s; a plain 8-bit library product with one scale 190), 4096 x
+// 4096 x 8192 with fp32 sums 270 (1020; the library's bfloat16 rate is 1350).  Two
+// workgroups share a CU, so that one works while the other meets at its
+// barrier or writes its results: a 256 x 256 tile of eight waves took 313 us.
 #include <type_traits>
 
 #include "dma_common.h"
@@ -37,7 +45,8 @@ struct Fp8Tile {
   static constexpr bool OWN_B = WAVES_M == 1;
   static constexpr int A_BYTES = BM * kBlockK, B_BYTES = BN * kBlockK;
   static constexpr int B_AT = STAGES * A_BYTES;
-  static constexpr int SCALES_AT = B_AT + (OWN_B ? 1 : STAGES) * B_BYTES;   // per stage: BM, then BN floats
+  // Scales, per stage BN, then BM floats.
+  static constexpr int SCALES_AT = B_AT + (OWN_B ? 1 : STAGES) * B_BYTES;
   static constexpr int SCALE_BYTES = 4 * (BM + BN);
   static constexpr int LDS_BYTES = SCALES_AT + STAGES * SCALE_BYTES;
   static constexpr int A_LOADS = BM / 8 / WAVES, B_LOADS = BN / 8 / WAVES;   // per wave, 1 KiB each
@@ -72,7 +81,8 @@ __device__ __forceinline__ void copy_slot(int v, int wave, int lane, int& row, i
 template <class T>
 __device__ __forceinline__ uint32_t copy_lds(int v, int wave, int t) {
   return v < T::A_LOADS ? t % T::STAGES * T::A_BYTES + (wave * T::A_LOADS + v) * 1024
-                        : T::B_AT + (T::OWN_B ? 0 : t % T::STAGES * T::B_BYTES) + (wave * T::B_LOADS + v - T::A_LOADS) * 1024;
+                        : T::B_AT + (T::OWN_B ? 0 : t % T::STAGES * T::B_BYTES) +
+                              (wave * T::B_LOADS + v - T::A_LOADS) * 1024;
 }
 
 // A pointer that is the same in every lane, in scalar registers.
@@ -384,7 +394,8 @@ fp8_tile_kernel(Fp8TileArgs p) {
       }
     }
     if constexpr (!LATE)   // (scales per row of B lie in the stage)
-      add<T>(total[T::FM - 1][T::FN - 1], sum[(BLOCKS - 1) & 1], scale[(BLOCKS - 1) & 1], sb_st + 32 * (T::FN - 1) + 4 * half);
+      add<T>(total[T::FM - 1][T::FN - 1], sum[(BLOCKS - 1) & 1], scale[(BLOCKS - 1) & 1],
+             sb_st + 32 * (T::FN - 1) + 4 * half);
     if (!T::DIRECT && t + 1 < kbs) {
       copy_scales(t + 1);
       asm volatile("" : "+v"(l));

@@ -20,7 +20,6 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 // of up to 16 bytes at any alignment, so rows of any length take the same code path.
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
-typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 constexpr int kBlockK = 128;   // columns that share one scale

@@ -7,10 +7,10 @@
 //
 // What bounds it are the chosen experts' weights, each of which is read once:
 // the tokens that chose an expert form the rows of one small product against
-// it.  A workgroup takes an expert and 16 NF rows of its weight; its eight waves
-// take an eighth of the columns each (consecutive ones: 7 % faster than every
-// eighth block of 128), read the weight straight into MFMA operands (16x16x32,
-// the tokens as the other operand) and add their fp32 sums in LDS.  Which
+// it.  A workgroup takes an expert and 16 NF rows of its weight; its waves take
+// equal shares of the columns (consecutive ones: 7 % faster than every eighth
+// block of 128), read the weight straight into MFMA operands (16x16x32, the
+// tokens as the other operand) and add their fp32 sums in LDS.  Which
 // experts there are is known on the device only, so the grids have a row for
 // every expert or for every token and slot, whichever is fewer, and workgroups
 // whose expert nobody chose, or another row takes, end at once.
@@ -20,6 +20,11 @@
 // top_k logits come before its own: one comparison per lane and ballot for 64
 // experts), beside workgroups that write the choice and its weights down; the
 // second product; the sum over a token's slots.  For one token the last two are one.
+//
+// Measured (us of kernel time; the card reads 6.2 TB/s): 64 tokens, 8 experts of 4096
+// x 14336 in bfloat16: 345 (5.5 TB/s) and 197 (4.8); 4 tokens, 64 experts of 4096 x
+// 1536 in e4m3: 72 (4.6) and 41 (4.1), logits 4.9, sum 4.7; one token, 8 experts
+// of 1024 x 512: 2.5, 6.8 and 4.7, latency throughout.
 //
 // The logits are summed in 64 bits: two experts' logits can lie closer than
 // fp32 sums of a few thousand terms resolve, and the choice between them is an
@@ -449,7 +454,8 @@ __device__ __forceinline__ void stream_blocks(int first, int end, int count, LW 
 
 // h for 16 NF inner columns of one expert and all its tokens (at most 16 MF).
 template <class E, bool FP8, bool GATED, int MF, int NF>
-__global__ void __launch_bounds__(64 * waves_of(MF)) __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_up_kernel(MoeArgs p) {
+__global__ void __launch_bounds__(64 * waves_of(MF))
+__attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_up_kernel(MoeArgs p) {
   constexpr int SIDES = GATED ? 2 : 1, W = waves_of(MF);
   __shared__ __attribute__((aligned(16))) float part[W / 2][SIDES * NF * MF][256];
   __shared__ int pair[kMaxTokens], slots[kMaxTokens], found;
@@ -591,7 +597,8 @@ __global__ void __launch_bounds__(64 * waves_of(MF)) __attribute__((amdgpu_waves
 
 // h W2 of 16 NF output columns of one expert and all its tokens, per pair.
 template <class E, bool FP8, int MF, int NF>
-__global__ void __launch_bounds__(64 * waves_of(MF)) __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_down_kernel(MoeArgs p) {
+__global__ void __launch_bounds__(64 * waves_of(MF))
+__attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_down_kernel(MoeArgs p) {
   constexpr int W = waves_of(MF);
   __shared__ __attribute__((aligned(16))) float part[W / 2][NF * MF][256];
   __shared__ int pair[kMaxTokens];

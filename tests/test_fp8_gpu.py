@@ -1,7 +1,8 @@
 """GPU tests of block quantisation and the block-scaled e4m3 product against their definitions.
 
 Quantisation is held to equality: scale and quotient are correctly rounded divisions, in fp32 for
-16-bit values and in 64 bits for fp32 ones, which the CPU forms too.  The product is held to a bound of its own roundings, with u = 2^-24:
+16-bit values and in 64 bits for fp32 ones, which the CPU forms too.  The product is held to a bound
+of its own roundings, with u = 2^-24:
   exact sums  - a block's 128 exact products are added in fp32 (at most 128 roundings), each block's
                 sum meets two roundings of its scale and one of its addition, eight partial totals are
                 added: (128 + blocks + 16) u of sum |s_a a s_b b|;
@@ -199,11 +200,15 @@ def check_product(M, N, K, type_="f32", act=0, bias=True, b_rows=128, fast=False
         d = torch.full((q.shape[0] * (K + pad) + offset,), 0x7F, dtype=torch.uint8, device="cuda")
         d[offset:].view(q.shape[0], K + pad)[:, :K] = q.view(torch.uint8).cuda()
         return d
-    dA, dB = padded(a), padded(b)
+    def scales(x):   # rows of 3 more values where the matrices are padded, NaN too
+        d = torch.full((x.shape[0], x.shape[1] + (3 if pad else 0)), float("nan"))
+        d[:, :x.shape[1]] = x
+        return d.cuda()
+    dA, dB, dSA, dSB = padded(a), padded(b), scales(sa), scales(sb)
     ldc = N + pad
     C = torch.full((M, ldc), 77.0, dtype=dtype, device="cuda")
-    lib.fp8_gemm_bias_act(M, N, K, alpha, dA.data_ptr() + offset, K + pad, sa.cuda(), M,
-                          dB.data_ptr() + offset, K + pad, sb.cuda(), sb.shape[1], b_rows,
+    lib.fp8_gemm_bias_act(M, N, K, alpha, dA.data_ptr() + offset, K + pad, dSA, dSA.shape[1],
+                          dB.data_ptr() + offset, K + pad, dSB, dSB.shape[1], b_rows,
                           None if bv is None else bv.cuda(), act, code, C, ldc, fast_sums=fast)
     torch.cuda.synchronize()
     got = C.cpu().double()
@@ -351,3 +356,27 @@ def test_offsets_past_31_bits():
     for i in range(3):
         got = X[i * ld:i * ld + 3].cpu().double()
         assert ((got - want[i]).abs() <= 2.0 ** -8 * want[i].abs() + 200 * U * 128).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1000, 3000, 777), (300, 2500, 1024), (2100, 2100, 256)])
+def test_tiles_by_the_rule(M, N, K):
+    """Enough tiles that the rule leaves the K-split kernels, by every way of summing and scaling."""
+    for fast in (False, True):
+        for b_rows in (1, 128):
+            check_product(M, N, K, "bf16", act=lib.ACT_GELU_TANH, b_rows=b_rows, fast=fast,
+                          pad=-K % 16, seed=M + b_rows)
+    check_product(M, N, K, "f16", fast=True, pad=1, offset=1, seed=M)
+
+
+def test_product_on_another_stream():
+    M, N, K = 70, 300, 512
+    a, sa, b, sb = operands(M, N, K, 128, 21)
+    dev = [t.cuda() for t in (a.view(torch.uint8), sa, b.view(torch.uint8), sb)]
+    out = [torch.empty((M, N), device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for C, stream in zip(out, (None, other)):
+        lib.fp8_gemm_bias_act(M, N, K, 1.0, dev[0], K, dev[1], M, dev[2], K, dev[3], 3, 128, None,
+                              lib.ACT_SILU, lib.TYPE_F32, C, N, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(*out)
