@@ -33,6 +33,9 @@
 // rounded to one such number they would cost as much accuracy as the final
 // rounding of Y, and the second MFMA is free beside the loads.  In binary16 hi
 // is clamped to +-65504, the type's range.
+// A 16-bit weight may be infinite; lo, of either sign or zero, would then turn an
+// infinite sum into NaN, which the sum of hi's products alone settles (high_sum,
+// add_low).
 #include <type_traits>
 
 #include "lm_common.h"
@@ -452,6 +455,31 @@ __device__ __forceinline__ void stream_blocks(int first, int end, int count, LW 
     run(std::integral_constant<int, MF>());
 }
 
+// Sums of the products of hi and of lo as one.
+__device__ __forceinline__ f32x4 add_low(f32x4 hi, f32x4 lo) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    hi[e] = __builtin_fabsf(hi[e]) < __builtin_inff() ? hi[e] + lo[e] : hi[e];
+  return hi;
+}
+
+// The sum of hi's products by one lane, for an element that came out NaN (sums
+// of their own in the loop, as one token's, would not fit the registers of wide tiles).
+// A NaN among the values ends it at once; only an infinite weight reads the row.
+template <class E>
+__device__ __forceinline__ float high_sum(const uint16_t* w, const uint16_t* hi, int n) {
+  float s = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < n && s == s; k += 8) {
+    const u32x4 a = load8h_upto(w + k, n - k), b = load8h_upto(hi + k, n - k);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      s = __builtin_fmaf(E::value((uint16_t)(a[i / 2] >> (16 * (i % 2)))),
+                         E::value((uint16_t)(b[i / 2] >> (16 * (i % 2)))), s);
+  }
+  return s;
+}
+
 // h for 16 NF inner columns of one expert and all its tokens (at most 16 MF).
 template <class E, bool FP8, bool GATED, int MF, int NF>
 __global__ void __launch_bounds__(64 * waves_of(MF))
@@ -693,7 +721,13 @@ __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_down_kernel(MoeArgs p)
     const int token = 16 * (f % MF) + (at / 4) % 16;
     const int col = n0 + 16 * (f / MF) + 4 * (at / 64) + at % 4;
     if (token >= rows.count || col >= D) continue;
-    p.part[(int64_t)pair[token] * D + col] = joined(part, f, at);
+    float y = joined(part, f, at);
+    if constexpr (!FP8) {
+      if (y != y)
+        y = high_sum<E>(static_cast<const uint16_t*>(p.W2) + ((int64_t)rows.expert * D + col) * p.ld2,
+                        p.h_hi + (int64_t)pair[token] * p.ldh, I);
+    }
+    p.part[(int64_t)pair[token] * D + col] = y;
   }
 }
 
@@ -740,6 +774,16 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) total[0][e] = __builtin_fmaf(v[e], f, total[0][e]);
   };
+  auto product = [&](const B& wb, const typename E::vec8 (&hi)[B::T],
+                     const typename E::vec8 (&lo)[B::T]) __attribute__((always_inline)) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, rest = v;
+#pragma unroll
+    for (int t = 0; t < B::T; ++t) {
+      v = E::mfma(wb.operand(t), hi[t], v);
+      rest = E::mfma(wb.operand(t), lo[t], rest);
+    }
+    return FP8 ? v + rest : add_low(v, rest);
+  };
   constexpr int AHEAD = FP8 ? 2 : 4;   // units whose loads are in flight together
   const int units = p.top_k * full, end = units * (wave + 1) / 8;
   for (int u0 = units * wave / 8; u0 < end; u0 += AHEAD) {
@@ -760,13 +804,7 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
       if (u0 + a >= end) break;
-      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int t = 0; t < B::T; ++t) {
-        v = E::mfma(wb[a].operand(t), lo[a][t], v);
-        v = E::mfma(wb[a].operand(t), hi[a][t], v);
-      }
-      add(v, (u0 + a) / full, (u0 + a) % full);
+      add(product(wb[a], hi[a], lo[a]), (u0 + a) / full, (u0 + a) % full);
     }
   }
   if (full * B::K < I) {
@@ -775,13 +813,13 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
     for (int s = wave; s < p.top_k; s += 8) {
       B wb;
       wb.load(row(s), tail);
-      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+      typename E::vec8 hi[B::T], lo[B::T];
 #pragma unroll
       for (int t = 0; t < B::T; ++t) {
-        v = E::mfma(wb.operand(t), B::tokens(p.h_lo + s * p.ldh, tail, t), v);
-        v = E::mfma(wb.operand(t), B::tokens(p.h_hi + s * p.ldh, tail, t), v);
+        hi[t] = B::tokens(p.h_hi + s * p.ldh, tail, t);
+        lo[t] = B::tokens(p.h_lo + s * p.ldh, tail, t);
       }
-      add(v, s, full);
+      add(product(wb, hi, lo), s, full);
     }
   }
   join(total, part, wave, lane);

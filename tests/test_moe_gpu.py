@@ -196,6 +196,27 @@ def test_nan_token_stays_in_its_row():
         assert torch.equal(m.y[t], clean[t]) and torch.equal(m.ids[t], ids[t])
 
 
+@pytest.mark.parametrize("T", [1, 3, 64])
+@pytest.mark.parametrize("type_,I,col", [("bf16", 45, 40), ("f16", 100, 3), ("bf16", 1000, 999)])
+def test_infinite_weight_reaches_its_column_alone(T, type_, I, col):
+    """h is held as two numbers, whose products with an infinite weight may differ in sign; the last
+    columns of an odd row are read twice, masked, and must count once."""
+    m = Layer(T, 77, I, 1, 1, type_, gated=False, act=lib.ACT_NONE, seed=13)
+    h = m.x.double() @ m.w1[0][col]
+    assert (h.abs() > 1e-4).all()     # (else a sign could be lost in rounding)
+    m.buffers()
+    m.call()
+    torch.cuda.synchronize()
+    clean = m.y[:, :77].clone()
+    m.d2[0, 9, col] = float("-inf")
+    m.call()
+    torch.cuda.synchronize()
+    got = m.y[:, :77]
+    assert torch.equal(got[:, 9].cpu().double(), -h.sign() * float("inf"))
+    got[:, 9] = clean[:, 9]
+    assert torch.equal(got, clean)
+
+
 def test_binary16_inner_range_is_clamped():
     m = Layer(1, 64, 16, 1, 1, "f16", gated=False, act=lib.ACT_NONE, seed=9)
     m.x[:] = 64.0
