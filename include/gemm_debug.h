@@ -50,6 +50,17 @@ extern "C" {
 int gemm_debug_force_tile(int op, int tile);
 
 /*
+ * Force how many rows of a weight a workgroup of moe_ffn's two products takes in
+ * later calls: 0 = by shape (the default), else 16, 32 or 64, reduced to the
+ * widest that the call's kernels have (the first product of a gated layer has 32,
+ * with E4M3 weights and more than 32 tokens 16; ungated with those 32; one
+ * token's second product always takes 16).  Returns GEMM_STATUS_INVALID_VALUE for
+ * another number.  Pure host state, not synchronised with calls in flight on
+ * other threads.
+ */
+int gemm_debug_force_moe_rows(int rows);
+
+/*
  * Force the number of K chunks (split-K) of later calls: op 0 = sgemm, op 1 =
  * the half products; splits -1 = choose by shape (the default), 1 = never
  * split, 2 .. 32 = that many chunks (still reduced to what K and the workspace

@@ -17,7 +17,8 @@ import os
 __all__ = ["GemmError", "gemm_create", "gemm_destroy", "sgemm", "sgemm_noalloc", "hgemm_bias_act",
            "bgemm_bias_act", "fp8_quantize", "fp8_gemm_bias_act", "MoeShape", "moe_ffn_workspace",
            "moe_ffn",
-           "gemm_status_string", "gemm_debug_force_tile", "gemm_debug_force_splits",
+           "gemm_status_string", "gemm_debug_force_tile", "gemm_debug_force_moe_rows",
+           "gemm_debug_force_splits",
            "gemm_debug_pick_config", "gemm_debug_use_tuned_table", "gemm_debug_force_swizzle",
            "gemm_debug_tile_map", "library_path",
            "load_library", "EXPORTED_SYMBOLS", "ACT_NONE", "ACT_GELU_TANH", "ACT_SILU",
@@ -46,7 +47,8 @@ TYPE_E4M3 = 3
 EXPORTED_SYMBOLS = ("gemm_create", "gemm_destroy", "sgemm", "sgemm_noalloc", "hgemm_bias_act",
                     "bgemm_bias_act", "fp8_quantize", "fp8_gemm_bias_act", "moe_ffn_workspace",
                     "moe_ffn",
-                    "gemm_status_string", "gemm_debug_force_tile", "gemm_debug_force_splits",
+                    "gemm_status_string", "gemm_debug_force_tile", "gemm_debug_force_moe_rows",
+                    "gemm_debug_force_splits",
                     "gemm_debug_pick_config", "gemm_debug_use_tuned_table",
                     "gemm_debug_force_swizzle", "gemm_debug_tile_map")
 
@@ -104,6 +106,8 @@ def load_library():
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_debug_force_tile.argtypes = [I, I]
     lib.gemm_debug_force_tile.restype = I
+    lib.gemm_debug_force_moe_rows.argtypes = [I]
+    lib.gemm_debug_force_moe_rows.restype = I
     lib.gemm_debug_force_splits.argtypes = [I, I]
     lib.gemm_debug_force_splits.restype = I
     IP = ctypes.POINTER(ctypes.c_int)
@@ -252,6 +256,10 @@ def gemm_status_string(status: int) -> str:
 
 def gemm_debug_force_tile(op: int, tile: int) -> int:
     return load_library().gemm_debug_force_tile(int(op), int(tile))
+
+
+def gemm_debug_force_moe_rows(rows: int) -> int:
+    return load_library().gemm_debug_force_moe_rows(int(rows))
 
 
 def gemm_debug_force_splits(op: int, splits: int) -> int:

@@ -2,9 +2,14 @@
 // include/gemm.h): argument checks, quick returns, and the launch.  None of
 // these calls allocates, copies to the host or uses the library's own
 // workspace, so all may be captured into a graph and run on any stream.
+#include <atomic>
+
+#include "../../include/gemm_debug.h"
 #include "lm_launch.h"
 
 namespace {
+
+std::atomic<int> g_force_moe_rows{0};
 
 bool ld_ok(int ld, int cols) { return ld >= (cols > 1 ? cols : 1); }
 int blocks(int n) { return (int)(((int64_t)n + 127) / 128); }
@@ -111,7 +116,13 @@ int moe_ffn(const moe_shape_t* shape, const uint16_t* X, int ldx, const uint16_t
   if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
   if (s.tokens == 0) return GEMM_STATUS_SUCCESS;
   const lasg::MoeCall c{s, X, ldx, R, ldr, W1, ld1, S1, W2, ld2, S2, ids, w, Y, ldy, workspace};
-  return finish(lasg::launch_moe(c, lasg::library_cus(), stream));
+  return finish(lasg::launch_moe(c, lasg::library_cus(), g_force_moe_rows.load(), stream));
+}
+
+int gemm_debug_force_moe_rows(int rows) {
+  if (rows != 0 && rows != 16 && rows != 32 && rows != 64) return GEMM_STATUS_INVALID_VALUE;
+  g_force_moe_rows.store(rows);
+  return GEMM_STATUS_SUCCESS;
 }
 
 }  // extern "C"

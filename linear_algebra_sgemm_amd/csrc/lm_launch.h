@@ -83,6 +83,7 @@ struct MoeCall {
   void* ws;
 };
 size_t moe_workspace_bytes(const moe_shape_t& s);
-hipError_t launch_moe(const MoeCall& c, int cus, hipStream_t s);
+// `force_rows`: rows of a weight per workgroup, 0 = by shape.
+hipError_t launch_moe(const MoeCall& c, int cus, int force_rows, hipStream_t s);
 
 }  // namespace lasg

@@ -70,6 +70,7 @@ MoeWorkspace moe_layout(const moe_shape_t& s) {
 struct MoeArgs {
   int tokens, d_model, d_ff, experts, top_k, act;
   bool norm, by_expert;   // by_expert: grid rows are experts, else (token, slot) pairs
+  int force_rows;         // rows of a weight per workgroup (host only; 0: by shape)
   const uint16_t* X;
   int64_t ldx;
   const uint16_t* R;
@@ -834,7 +835,8 @@ namespace {
 
 // Tiles of 16 NF rows: the widest that leaves two workgroups per compute unit
 // (tokens are read once per workgroup, and its start and end cost a few microseconds).
-int row_tiles(int64_t n, int64_t grid_rows, int widest, int cus) {
+int row_tiles(int64_t n, int64_t grid_rows, int widest, int cus, int force_rows) {
+  if (force_rows != 0) return force_rows / 16 < widest ? force_rows / 16 : widest;
   int nf = widest;
   while (nf > 1 && (n + 16 * nf - 1) / (16 * nf) * grid_rows < 2 * cus) nf /= 2;
   return nf;
@@ -857,7 +859,7 @@ hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s)
   };
   // (With e4m3 weights and 64 tokens the widest tile does not fit the registers.)
   constexpr int WIDE = FP8 && MF == 4 ? 2 : 4;
-  const int up = row_tiles(a.d_ff, rows, gated ? WIDE / 2 : WIDE, cus);
+  const int up = row_tiles(a.d_ff, rows, gated ? WIDE / 2 : WIDE, cus, a.force_rows);
   const auto launch_up = [&](auto is_gated, auto nf) {
     constexpr int NF = decltype(nf)::value;
     moe_up_kernel<E, FP8, decltype(is_gated)::value, MF, NF>
@@ -878,7 +880,7 @@ hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s)
     moe_down_token_kernel<E, FP8><<<grid(a.d_model, 1, 1), 512, 0, s>>>(a);
     return hipGetLastError();
   }
-  const int down = row_tiles(a.d_model, rows, 4, cus);
+  const int down = row_tiles(a.d_model, rows, 4, cus, a.force_rows);
   if (down == 4)
     moe_down_kernel<E, FP8, MF, 4><<<grid(a.d_model, 4, up_rows), 64 * waves_of(MF), 0, s>>>(a);
   else if (down == 2)
@@ -901,7 +903,7 @@ hipError_t launch_moe_as(const MoeArgs& a, bool gated, int cus, hipStream_t s) {
 
 size_t moe_workspace_bytes(const moe_shape_t& s) { return moe_layout(s).bytes; }
 
-hipError_t launch_moe(const MoeCall& c, int cus, hipStream_t s) {
+hipError_t launch_moe(const MoeCall& c, int cus, int force_rows, hipStream_t s) {
   const moe_shape_t& sh = c.shape;
   const MoeWorkspace l = moe_layout(sh);
   uint8_t* ws = static_cast<uint8_t*>(c.ws);
@@ -914,6 +916,7 @@ hipError_t launch_moe(const MoeCall& c, int cus, hipStream_t s) {
   a.act = sh.act;
   a.norm = sh.norm_topk != 0;
   a.by_expert = sh.experts <= sh.tokens * sh.top_k || sh.experts > kPairExperts;
+  a.force_rows = force_rows;
   a.X = c.X;
   a.ldx = c.ldx;
   a.R = c.R;
