@@ -19,9 +19,11 @@
 // 4096 weights went to the wrong side of the middle between two e4m3 numbers.
 // The 64-bit quotient reaches the conversion as an fp32 number whose last bit
 // stands for everything below it, so that nothing is lost before it.  16-bit
-// inputs gain nothing from that (their quotients meet such a middle exactly or
-// stay clear of it by far more than an fp32 rounding) and pay: 4096 x 14336 both
-// ways 57 us against 81, bound by the vector unit instead of by memory.
+// inputs would pay for that: 4096 x 14336 both ways 81 us against 57, bound by the
+// vector unit instead of by memory.  What they give up: exact quotients stay clear of
+// such a middle by far more than an fp32 rounding or lie on it, and where they
+// lie on it the rounded scale moves some off it, to either side (one pair
+// of bfloat16 significands in about 10^4; half a step of e4m3 either way).
 #include "lm_common.h"
 #include "lm_launch.h"
 
