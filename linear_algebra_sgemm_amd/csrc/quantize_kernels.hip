@@ -11,9 +11,10 @@
 // keeps 1 / s finite; a block of zeros has s = 2^-126 and values 0.
 //
 // The quotient comes from the block's correctly rounded reciprocal r: q0 = x r,
-// then q = q0 + r (x - q0 s) with fused multiply-adds, which is x / s correctly
+// then q = q0 - r (q0 s - x) with fused multiply-adds, which is x / s correctly
 // rounded (Markstein's theorem) unless the remainder underflows, where the
 // quotient is far below e4m3's smallest value.  Three operations instead of a division's ten.
+// (The remainder with this sign leaves -0 as it is; x - q0 s, added, gave +0.)
 // For 16-bit inputs scale and quotient are fp32 numbers.  For fp32 inputs
 // they are formed in 64 bits and rounded once: rounded twice, one or two of 4096 x
 // 4096 weights went to the wrong side of the middle between two e4m3 numbers.
@@ -123,7 +124,7 @@ struct Scale {
   }
   __device__ __forceinline__ float operator()(float x) const {
     const float q = x * r;
-    return __builtin_fmaf(__builtin_fmaf(-q, sc, x), r, q);
+    return __builtin_fmaf(-__builtin_fmaf(q, sc, -x), r, q);
   }
 };
 template <>
@@ -139,7 +140,7 @@ struct Scale<GEMM_TYPE_F32> {
   }
   __device__ __forceinline__ float operator()(float x) const {
     const double q0 = (double)x * r;
-    const double q = __builtin_fma(__builtin_fma(-q0, sc, (double)x), r, q0);
+    const double q = __builtin_fma(-__builtin_fma(q0, sc, -(double)x), r, q0);
     const uint64_t bits = __builtin_bit_cast(uint64_t, q);
     const uint32_t lo = (uint32_t)bits, below = lo & 0x1fffffffu;   // what fp32 does not hold
     const uint32_t odd = (lo & 0xe0000000u) | (below != 0 ? 0x20000000u : 0u);
