@@ -12,9 +12,11 @@
 //
 // The quotient comes from the block's correctly rounded reciprocal r: q0 = x r,
 // then q = q0 - r (q0 s - x) with fused multiply-adds, which is x / s correctly
-// rounded (Markstein's theorem) unless the remainder underflows, where the
-// quotient is far below e4m3's smallest value.  Three operations instead of a division's ten.
-// (The remainder with this sign leaves -0 as it is; x - q0 s, added, gave +0.)
+// rounded (Markstein's theorem) unless the remainder underflows.  Three operations instead
+// of a division's ten.  (The remainder with this sign leaves -0 as it is; x - q0 s,
+// added, gave +0.)  Quotients that e4m3 does not round to 0 are above 2^-10, their
+// remainders multiples of 2^-57 s: representable for s >= 2^-60.  Only bfloat16 has smaller
+// blocks of 16-bit values; there x and s are first multiplied by 2^64, exactly.
 // For 16-bit inputs scale and quotient are fp32 numbers.  For fp32 inputs
 // they are formed in 64 bits and rounded once: rounded twice, one or two of 4096 x
 // 4096 weights went to the wrong side of the middle between two e4m3 numbers.
@@ -115,14 +117,16 @@ __device__ __forceinline__ uint32_t max16(uint32_t x) {
 // no remainder step: infinity times zero.)
 template <int TYPE>
 struct Scale {
-  float s, r, sc;
+  float s, r, sc, up;
   __device__ __forceinline__ explicit Scale(float amax) {
     s = amax / (float)kE4m3Max;
     if (s < (float)kMinScale) s = (float)kMinScale;   // (false for NaN)
-    r = 1.0f / s;
-    sc = __builtin_fabsf(s) < __builtin_inff() ? s : 0.0f;
+    up = TYPE == GEMM_TYPE_BF16 && s < 0x1p-60f ? 0x1p64f : 1.0f;
+    r = 1.0f / (s * up);
+    sc = __builtin_fabsf(s) < __builtin_inff() ? s * up : 0.0f;
   }
   __device__ __forceinline__ float operator()(float x) const {
+    if constexpr (TYPE == GEMM_TYPE_BF16) x *= up;
     const float q = x * r;
     return __builtin_fmaf(-__builtin_fmaf(q, sc, -x), r, q);
   }
