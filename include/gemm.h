@@ -221,8 +221,9 @@ int moe_ffn_workspace(const moe_shape_t* shape, size_t* bytes);
  * S1[e][d / 128][row / 128], S2[e][i / 128][d / 128], dense; else they are
  * ignored.  Columns past D or I of a row are not used.
  * The logits and the choice are computed in 64 bits, products with fp32 sums;
- * h is kept as two numbers of `type`, so in F16 its range is +-65504 (larger
- * finite values are clamped to that).
+ * h is kept as two numbers of `type`: in BF16 to 2^-17 of itself, in F16 to 2^-17
+ * of a token's largest |h| for that expert or better, and in F16 its range is
+ * +-65504 (larger finite values are clamped to that).
  * `workspace` (256-byte aligned, at least moe_ffn_workspace bytes) belongs to
  * the call until its work on `stream` is done; its contents need no
  * preparation.  tokens == 0: nothing is done.

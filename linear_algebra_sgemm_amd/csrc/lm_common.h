@@ -114,6 +114,7 @@ struct LmF16 {
   }
   // Largest finite value: inner activations are clamped to it (see moe_kernels.hip).
   static constexpr float kMax = 65504.0f;
+  static constexpr bool kNarrow = true;   // fewer exponents than fp32
 };
 struct LmBF16 {
   typedef bf16x8 vec8;
@@ -128,6 +129,7 @@ struct LmBF16 {
     return __builtin_bit_cast(float, (uint32_t)b << 16);
   }
   static constexpr float kMax = 3.3895313892515355e38f;
+  static constexpr bool kNarrow = false;
 };
 
 // x times a factor: GELU in its tanh form is x / (1 + exp(-2u)) with u =

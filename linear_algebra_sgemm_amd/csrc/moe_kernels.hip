@@ -31,8 +31,16 @@
 // output.  The inner activations h are kept to about 16 (bfloat16) or 22
 // (binary16) bits as a pair hi + lo of the 16-bit type, each multiplied by W2:
 // rounded to one such number they would cost as much accuracy as the final
-// rounding of Y, and the second MFMA is free beside the loads.  In binary16 hi
-// is clamped to +-65504, the type's range.
+// rounding of Y, and the second MFMA is free beside the loads.  In binary16 h
+// is clamped to +-65504, the type's range, and the pair cannot hold less than
+// 2^-24.  Rows (a token's h for one expert) whose largest |h| is at least kSmallPeak
+// lose at most 2^-17 of that by it and are taken as they are.  For the others the
+// second product reads h in fp32, which the first writes beside the pair, with the
+// largest |h| of every workgroup's columns, and multiplies it by a power of two that brings
+// the row's largest to 2^14 .. 2^15: 2^-39 of it is lost.  Such rows take 10 to 20 %
+// longer (4 tokens, 64 e4m3 experts: 121 us for 109), the others what the extra
+// stores cost, up to half a microsecond in each product.  (Plain stores: one
+// atomic maximum per row and workgroup took up to 8 us of the first product.)
 // A 16-bit weight may be infinite; lo, of either sign or zero, would then turn an
 // infinite sum into NaN, which the sum of hi's products alone settles (high_sum,
 // add_low).
@@ -47,10 +55,11 @@ namespace {
 
 constexpr int kMaxTokens = 64;   // one wave's lanes hold the tokens
 constexpr int kMaxExperts = 1024, kMaxSlots = 32;   // (as lm_capi.cpp allows)
+constexpr uint32_t kSmallPeak = 0x3b800000u;   // 2^-8, as the bits of an fp32 number
 
 // Where the parts of the workspace lie (bytes).
 struct MoeWorkspace {
-  size_t logits, h, part, bytes;
+  size_t logits, h, part, wide, flags, peaks, bytes;
   int ldh;   // elements per row of h_hi, h_lo
 };
 
@@ -63,7 +72,12 @@ MoeWorkspace moe_layout(const moe_shape_t& s) {
   w.logits = 0;
   w.h = round256((size_t)s.tokens * s.experts * sizeof(double));
   w.part = w.h + round256(2 * pairs * w.ldh * sizeof(uint16_t));
-  w.bytes = w.part + round256(pairs * s.d_model * sizeof(float));
+  w.wide = w.part + round256(pairs * s.d_model * sizeof(float));
+  const bool narrow = s.type == GEMM_TYPE_F16;
+  w.flags = w.wide + (narrow ? round256(pairs * w.ldh * sizeof(float)) : 0);
+  w.peaks = w.flags + (narrow ? round256(2 * pairs * sizeof(uint32_t)) : 0);
+  w.bytes = w.peaks +
+            (narrow ? round256(pairs * (((size_t)s.d_ff + 15) / 16) * sizeof(uint32_t)) : 0);
   return w;
 }
 
@@ -89,8 +103,51 @@ struct MoeArgs {
   uint16_t* h_hi;
   uint16_t* h_lo;
   int64_t ldh;
+  // Binary16 only: h in fp32 (rows of ldh); for every row whether some |h| is at least
+  // kSmallPeak, and whether some workgroup's largest is below it and not zero;
+  // the largest |h| (bits) of each of the first product's up_tiles workgroups.
+  float* h_wide;
+  uint32_t* flags;
+  uint32_t* peaks;
+  int up_tiles;
   float* part;
 };
+
+// Whether a row needs the fp32 values.
+__device__ __forceinline__ bool small_row(const MoeArgs& p, int pair) {
+  const u32x2 f = *reinterpret_cast<const u32x2*>(p.flags + 2 * pair);
+  return f[0] == 0 && f[1] != 0;
+}
+// The largest |h| (bits) of a row, by one wave, in every lane.
+__device__ __forceinline__ uint32_t row_peak(const MoeArgs& p, int pair) {
+  uint32_t m = 0;
+  for (int b = threadIdx.x % kWave; b < p.up_tiles; b += kWave) {
+    const uint32_t x = p.peaks[(int64_t)pair * p.up_tiles + b];
+    m = m > x ? m : x;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t x = (uint32_t)__shfl_xor((int)m, d);
+    m = m > x ? m : x;
+  }
+  return m;
+}
+// The exponent of the power of two that a row is multiplied by (negated: divided by), as a factor.
+__device__ __forceinline__ int row_shift(uint32_t peak) {
+  const int up = 141 - (int)(peak >> 23);   // 2^14 over the largest's exponent
+  return peak == 0 || peak >= kSmallPeak ? 0 : up < 126 ? up : 126;
+}
+__device__ __forceinline__ float power_of_two(int e) {
+  return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+}
+
+// h as hi + lo.
+template <class E>
+__device__ __forceinline__ void split(float h, uint16_t& hi, uint16_t& lo) {
+  const bool inf = __builtin_fabsf(h) == __builtin_inff();
+  hi = E::bits(h);
+  lo = E::bits(inf ? 0.0f : h - E::value(hi));
+}
 
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
@@ -226,17 +283,21 @@ __device__ __forceinline__ void route_token(const MoeArgs& p, int t, double* key
 // for a (token, slot) pair: then the expert's first pair does the work.
 struct Rows {
   int expert, count;   // count == 0: nothing for this workgroup
+  bool small;          // NARROW: whether one of them is a small row
 };
+template <bool NARROW>
 __device__ __forceinline__ Rows rows_from_ids(const MoeArgs& p, int grid_row, int* pair) {
   const int lane = threadIdx.x % kWave;
   const int pairs = p.tokens * p.top_k;
-  Rows out{p.by_expert ? grid_row : p.ids[grid_row], 0};
+  Rows out{p.by_expert ? grid_row : p.ids[grid_row], 0, false};
   for (int q0 = 0; q0 < pairs; q0 += 4 * kWave) {   // (pairs are in token order)
     int id[4];
+    bool small[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int q = q0 + u * kWave + lane;
       id[u] = q < pairs ? p.ids[q] : -1;
+      small[u] = NARROW && q < pairs ? small_row(p, q) : false;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -244,10 +305,11 @@ __device__ __forceinline__ Rows rows_from_ids(const MoeArgs& p, int grid_row, in
       if (mask == 0) continue;
       if (!p.by_expert && out.count == 0 &&
           q0 + u * kWave + __ffsll((unsigned long long)mask) - 1 != grid_row)
-        return Rows{out.expert, 0};
+        return Rows{out.expert, 0, false};
       if (threadIdx.x < kWave && id[u] == out.expert)
         pair[out.count + __popcll(mask & ((uint64_t(1) << lane) - 1))] = q0 + u * kWave + lane;
       out.count += __popcll(mask);
+      if (NARROW && __ballot(id[u] == out.expert && small[u]) != 0) out.small = true;
     }
   }
   if (out.count > 0) __syncthreads();
@@ -330,6 +392,28 @@ struct Block {
                               : load16(row + at);
     return __builtin_bit_cast(vec8, x & tail.mask[t]);
   }
+  // Eight fp32 values times `factor` as two numbers of the type.
+  static __device__ __forceinline__ void split8(const float* at, float factor, vec8& hi, vec8& lo) {
+    const f32x4 x[2] = {*reinterpret_cast<const f32x4_any*>(at),
+                        *reinterpret_cast<const f32x4_any*>(at + 4)};
+    uint16_t h[8], l[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split<E>(x[e / 4][e % 4] * factor, h[e], l[e]);
+    hi = __builtin_bit_cast(vec8, h);
+    lo = __builtin_bit_cast(vec8, l);
+  }
+  // The tokens from a row of h_wide.  (Its rows are padded to 128 columns, so what a tail's
+  // mask takes away may be read.)
+  static __device__ __forceinline__ void tokens(const float* row, float factor, int k0, int g, int t,
+                                                vec8& hi, vec8& lo) {
+    split8(row + k0 + chunk(t / PER, g) + 8 * (t % PER), factor, hi, lo);
+  }
+  static __device__ __forceinline__ void tokens(const float* row, float factor, const Tail& tail,
+                                                int t, vec8& hi, vec8& lo) {
+    split8(row + tail.at[t / PER] + 8 * (t % PER), factor, hi, lo);
+    hi = __builtin_bit_cast(vec8, __builtin_bit_cast(u32x4, hi) & tail.mask[t]);
+    lo = __builtin_bit_cast(vec8, __builtin_bit_cast(u32x4, lo) & tail.mask[t]);
+  }
   // The first `bytes` (fewer than 32) bytes of a row, up to 16.
   static __device__ __forceinline__ u32x4 gather(const uint8_t* row, int bytes) {
     uint64_t lo = 0, hi = 0;
@@ -352,6 +436,8 @@ __global__ void __launch_bounds__(256) moe_logits_kernel(MoeArgs p) {
   __shared__ double sums[4][TT];
   const int e = blockIdx.x, t0 = TT * blockIdx.y;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  if (E::kNarrow && blockIdx.x == 0 && blockIdx.y == 0)
+    for (int q = threadIdx.x; q < 2 * p.tokens * p.top_k; q += 256) p.flags[q] = 0;
   const uint16_t* r = p.R + e * p.ldr;
   double acc[TT] = {};
   for (int d = 8 * threadIdx.x; d < p.d_model; d += 8 * 256) {
@@ -467,6 +553,14 @@ __device__ __forceinline__ f32x4 add_low(f32x4 hi, f32x4 lo) {
 // The sum of hi's products by one lane, for an element that came out NaN (sums
 // of their own in the loop, as one token's, would not fit the registers of wide tiles).
 // A NaN among the values ends it at once; only an infinite weight reads the row.
+// In binary16 it is the sum of h itself, whose hi may be zero where h is not.
+template <class E>
+__device__ __forceinline__ float high_sum(const uint16_t* w, const float* h, int n) {
+  float s = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < n && s == s; ++k) s = __builtin_fmaf(E::value(w[k]), h[k], s);
+  return s;
+}
 template <class E>
 __device__ __forceinline__ float high_sum(const uint16_t* w, const uint16_t* hi, int n) {
   float s = 0.0f;
@@ -489,6 +583,7 @@ __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_up_kernel(MoeArgs p) {
   __shared__ __attribute__((aligned(16))) float part[W / 2][SIDES * NF * MF][256];
   __shared__ int pair[kMaxTokens], slots[kMaxTokens], found;
   __shared__ double key[kMaxExperts], chosen[kMaxSlots];
+  __shared__ uint32_t peak[E::kNarrow ? kMaxTokens : 1];
   if (blockIdx.y == gridDim.y - 1) {   // (one grid row past the experts: the tokens' choices)
     for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) route_token<W>(p, t, key, chosen);
     return;
@@ -601,6 +696,7 @@ __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_up_kernel(MoeArgs p) {
       multiply(wb, t, i, full);
     }
   }
+  if (E::kNarrow && threadIdx.x < kMaxTokens) peak[threadIdx.x] = 0;
   join(total, part, wave, lane);
   for (int v = threadIdx.x; v < NF * MF * 256; v += 64 * W) {
     const int f = v / 256, at = v % 256;
@@ -617,10 +713,24 @@ __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_up_kernel(MoeArgs p) {
     if constexpr (GATED) h *= s[SIDES - 1];
     const bool inf = __builtin_fabsf(h) == __builtin_inff();   // (infinities and NaN stay)
     if (!inf) h = h > E::kMax ? E::kMax : h < -E::kMax ? -E::kMax : h;
-    const uint16_t hi = E::bits(h);
     const int64_t at_h = (int64_t)pair[token] * p.ldh + n;
-    p.h_hi[at_h] = hi;
-    p.h_lo[at_h] = E::bits(inf ? 0.0f : h - E::value(hi));
+    split<E>(h, p.h_hi[at_h], p.h_lo[at_h]);
+    if constexpr (E::kNarrow) {
+      p.h_wide[at_h] = h;
+      atomicMax(&peak[token], __builtin_bit_cast(uint32_t, h) & 0x7fffffffu);
+    }
+  }
+  if constexpr (E::kNarrow) {
+    __syncthreads();
+    if ((int)threadIdx.x < count) {
+      const int q = pair[threadIdx.x];
+      const uint32_t m = peak[threadIdx.x];
+      p.peaks[(int64_t)q * gridDim.x + blockIdx.x] = m;
+      if (m >= kSmallPeak)
+        p.flags[2 * q] = 1;
+      else if (m != 0)
+        p.flags[2 * q + 1] = 1;
+    }
   }
 }
 
@@ -630,8 +740,8 @@ __global__ void __launch_bounds__(64 * waves_of(MF))
 __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_down_kernel(MoeArgs p) {
   constexpr int W = waves_of(MF);
   __shared__ __attribute__((aligned(16))) float part[W / 2][NF * MF][256];
-  __shared__ int pair[kMaxTokens];
-  const Rows rows = rows_from_ids(p, blockIdx.y, pair);
+  __shared__ int pair[kMaxTokens], shift[E::kNarrow ? kMaxTokens : 1];
+  const Rows rows = rows_from_ids<E::kNarrow>(p, blockIdx.y, pair);
   if (rows.count == 0) return;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -683,21 +793,77 @@ __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_down_kernel(MoeArgs p)
     }
   };
   const int full = I / B::K;
-  stream_blocks<MF, NF, FP8 ? 1 : 2, !FP8, B, X>(
-      full * wave / W, full * (wave + 1) / W, rows.count,
-      [&](B (&wb)[NF], int kb) __attribute__((always_inline)) {
+  auto load_weights = [&](B (&wb)[NF], int kb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < NF; ++j) wb[j].load(w[j], kb * B::K, g);
-      },
-      [&](X& t, int i, int kb) __attribute__((always_inline)) {
+    for (int j = 0; j < NF; ++j) wb[j].load(w[j], kb * B::K, g);
+  };
+  auto block_scale = [&](int kb) __attribute__((always_inline)) {
+    return FP8 ? uniform_value(scale + kb * rbs) : 1.0f;
+  };
+  const int first = full * wave / W, end = full * (wave + 1) / W;
+  const bool small = E::kNarrow && rows.small;
+  float factor[E::kNarrow ? MF : 1];
+  if (!small) {
+    stream_blocks<MF, NF, FP8 ? 1 : 2, !FP8, B, X>(
+        first, end, rows.count, load_weights,
+        [&](X& t, int i, int kb) __attribute__((always_inline)) {
+#pragma unroll
+          for (int m = 0; m < B::T; ++m) {
+            t.hi[m] = B::tokens(p.h_hi + h_row[i], kb * B::K, g, m);
+            t.lo[m] = B::tokens(p.h_lo + h_row[i], kb * B::K, g, m);
+          }
+          t.scale = block_scale(kb);
+        },
+        multiply);
+  } else if constexpr (E::kNarrow) {
+    // h in fp32, for a workgroup with a small row: a block at a time, the values of one
+    // MFMA after the other (all of a block's would not fit the registers).  The products
+    // of the other rows are added in the same order and give the same bits.
+    for (int t = wave; t < rows.count; t += W) {
+      const int s = row_shift(row_peak(p, pair[t]));
+      if (lane == 0) shift[t] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+      factor[i] = power_of_two(shift[16 * i + r < rows.count ? 16 * i + r : rows.count - 1]);
+#pragma unroll 1
+    for (int kb = first; kb < end; ++kb) {
+      B wb[NF];
+      load_weights(wb, kb);
+      const float s = block_scale(kb);
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        if (16 * i >= rows.count) break;
+        f32x4 v[NF];
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+          v[j] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : total[j * MF + i];
 #pragma unroll
         for (int m = 0; m < B::T; ++m) {
-          t.hi[m] = B::tokens(p.h_hi + h_row[i], kb * B::K, g, m);
-          t.lo[m] = B::tokens(p.h_lo + h_row[i], kb * B::K, g, m);
+          typename E::vec8 hi, lo;
+          B::tokens(p.h_wide + h_row[i], factor[i], kb * B::K, g, m, hi, lo);
+#pragma unroll
+          for (int j = 0; j < NF; ++j) {
+            const typename E::vec8 a = wb[j].operand(m);
+            v[j] = E::mfma(a, lo, v[j]);
+            v[j] = E::mfma(a, hi, v[j]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        t.scale = FP8 ? uniform_value(scale + kb * rbs) : 1.0f;
-      },
-      multiply);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          f32x4& sum = total[j * MF + i];
+          if constexpr (FP8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(v[j][e], s, sum[e]);
+          } else {
+            sum = v[j];
+          }
+        }
+      }
+    }
+  }
   if (full * B::K < I && wave == W - 1) {
     const typename B::Tail tail(full * B::K, I, g);
     B wb[NF];
@@ -709,10 +875,14 @@ __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_down_kernel(MoeArgs p)
       X t;
 #pragma unroll
       for (int m = 0; m < B::T; ++m) {
-        t.hi[m] = B::tokens(p.h_hi + h_row[i], tail, m);
-        t.lo[m] = B::tokens(p.h_lo + h_row[i], tail, m);
+        if (!small) {
+          t.hi[m] = B::tokens(p.h_hi + h_row[i], tail, m);
+          t.lo[m] = B::tokens(p.h_lo + h_row[i], tail, m);
+        } else if constexpr (E::kNarrow) {
+          B::tokens(p.h_wide + h_row[i], factor[i], tail, m, t.hi[m], t.lo[m]);
+        }
       }
-      t.scale = FP8 ? uniform_value(scale + full * rbs) : 1.0f;
+      t.scale = block_scale(full);
       multiply(wb, t, i, full);
     }
   }
@@ -723,10 +893,17 @@ __attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : 2))) moe_down_kernel(MoeArgs p)
     const int col = n0 + 16 * (f / MF) + 4 * (at / 64) + at % 4;
     if (token >= rows.count || col >= D) continue;
     float y = joined(part, f, at);
+    if (small) y *= power_of_two(-shift[E::kNarrow ? token : 0]);
     if constexpr (!FP8) {
-      if (y != y)
-        y = high_sum<E>(static_cast<const uint16_t*>(p.W2) + ((int64_t)rows.expert * D + col) * p.ld2,
-                        p.h_hi + (int64_t)pair[token] * p.ldh, I);
+      const int64_t h_at = (int64_t)pair[token] * p.ldh;
+      const uint16_t* w_at =
+          static_cast<const uint16_t*>(p.W2) + ((int64_t)rows.expert * D + col) * p.ld2;
+      if (y != y) {
+        if constexpr (E::kNarrow)
+          y = high_sum<E>(w_at, p.h_wide + h_at, I);
+        else
+          y = high_sum<E>(w_at, p.h_hi + h_at, I);
+      }
     }
     p.part[(int64_t)pair[token] * D + col] = y;
   }
@@ -761,7 +938,8 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
   const int64_t rbs = (D + 127) / 128;
   const int kbs = (I + 127) / 128, full = I / B::K;
   const int mine = p.ids[lane < p.top_k ? lane : 0];
-  const float weight = p.w[lane < p.top_k ? lane : 0];
+  float weight = p.w[lane < p.top_k ? lane : 0];
+  const bool small = E::kNarrow && small_row(p, lane < p.top_k ? lane : 0);
   f32x4 total[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
   auto row = [&](int s) __attribute__((always_inline)) {
     const int expert = __builtin_amdgcn_readlane(mine, s);
@@ -785,43 +963,74 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
     }
     return FP8 ? v + rest : add_low(v, rest);
   };
-  constexpr int AHEAD = FP8 ? 2 : 4;   // units whose loads are in flight together
   const int units = p.top_k * full, end = units * (wave + 1) / 8;
-  for (int u0 = units * wave / 8; u0 < end; u0 += AHEAD) {
-    B wb[AHEAD];
-    typename E::vec8 hi[AHEAD][B::T], lo[AHEAD][B::T];
+  // SMALL: some slot's row is small, h is taken in fp32 (a unit at a time).
+  auto products = [&](auto is_small) __attribute__((always_inline)) {
+    constexpr bool SMALL = decltype(is_small)::value;
+    constexpr int AHEAD = SMALL ? 1 : FP8 ? 2 : 4;   // units whose loads are in flight together
+    int shift = 0;   // lane s: of slot s
+    if constexpr (SMALL) {
+      for (int s = 0; s < p.top_k; ++s) {
+        const int x = row_shift(row_peak(p, s));
+        if (lane == s) shift = x;
+      }
+      weight *= power_of_two(-shift);
+    }
+    auto factor = [&](int s) __attribute__((always_inline)) {
+      return power_of_two(__builtin_amdgcn_readlane(shift, s));
+    };
+    for (int u0 = units * wave / 8; u0 < end; u0 += AHEAD) {
+      B wb[AHEAD];
+      typename E::vec8 hi[AHEAD][B::T], lo[AHEAD][B::T];
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      const int u = u0 + a < end ? u0 + a : end - 1;
-      const int s = u / full, kb = u % full;
-      wb[a].load(row(s), kb * B::K, g);
+      for (int a = 0; a < AHEAD; ++a) {
+        const int u = u0 + a < end ? u0 + a : end - 1;
+        const int s = u / full, kb = u % full;
+        wb[a].load(row(s), kb * B::K, g);
 #pragma unroll
-      for (int t = 0; t < B::T; ++t) {
-        hi[a][t] = B::tokens(p.h_hi + s * p.ldh, kb * B::K, g, t);
-        lo[a][t] = B::tokens(p.h_lo + s * p.ldh, kb * B::K, g, t);
+        for (int t = 0; t < B::T; ++t) {
+          if constexpr (SMALL) {
+            B::tokens(p.h_wide + s * p.ldh, factor(s), kb * B::K, g, t, hi[a][t], lo[a][t]);
+          } else {
+            hi[a][t] = B::tokens(p.h_hi + s * p.ldh, kb * B::K, g, t);
+            lo[a][t] = B::tokens(p.h_lo + s * p.ldh, kb * B::K, g, t);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);   // (all issued before anything waits)
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        if (u0 + a >= end) break;
+        add(product(wb[a], hi[a], lo[a]), (u0 + a) / full, (u0 + a) % full);
       }
     }
-    __builtin_amdgcn_sched_barrier(0);   // (all issued before anything waits)
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      if (u0 + a >= end) break;
-      add(product(wb[a], hi[a], lo[a]), (u0 + a) / full, (u0 + a) % full);
-    }
-  }
-  if (full * B::K < I) {
-    const typename B::Tail tail(full * B::K, I, g);
+    if (full * B::K < I) {
+      const typename B::Tail tail(full * B::K, I, g);
 #pragma unroll 1
-    for (int s = wave; s < p.top_k; s += 8) {
-      B wb;
-      wb.load(row(s), tail);
-      typename E::vec8 hi[B::T], lo[B::T];
+      for (int s = wave; s < p.top_k; s += 8) {
+        B wb;
+        wb.load(row(s), tail);
+        typename E::vec8 hi[B::T], lo[B::T];
 #pragma unroll
-      for (int t = 0; t < B::T; ++t) {
-        hi[t] = B::tokens(p.h_hi + s * p.ldh, tail, t);
-        lo[t] = B::tokens(p.h_lo + s * p.ldh, tail, t);
+        for (int t = 0; t < B::T; ++t) {
+          if constexpr (SMALL) {
+            B::tokens(p.h_wide + s * p.ldh, factor(s), tail, t, hi[t], lo[t]);
+          } else {
+            hi[t] = B::tokens(p.h_hi + s * p.ldh, tail, t);
+            lo[t] = B::tokens(p.h_lo + s * p.ldh, tail, t);
+          }
+        }
+        add(product(wb, hi, lo), s, full);
       }
-      add(product(wb, hi, lo), s, full);
     }
+  };
+  if constexpr (E::kNarrow) {
+    if (__ballot(small) != 0)
+      products(std::true_type());
+    else
+      products(std::false_type());
+  } else {
+    products(std::false_type());
   }
   join(total, part, wave, lane);
   if (threadIdx.x < 16 && n0 + (int)threadIdx.x < D) {
@@ -843,7 +1052,7 @@ int row_tiles(int64_t n, int64_t grid_rows, int widest, int cus, int force_rows)
 }
 
 template <class E, bool FP8, int MF>
-hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s) {
+hipError_t launch_moe_rows(MoeArgs a, bool gated, int cus, hipStream_t s) {
   const int pairs = a.tokens * a.top_k;
   const int rows = a.experts < pairs ? a.experts : pairs;   // experts at work, at most
   if (a.tokens == 1)
@@ -862,6 +1071,7 @@ hipError_t launch_moe_rows(const MoeArgs& a, bool gated, int cus, hipStream_t s)
   const int up = row_tiles(a.d_ff, rows, gated ? WIDE / 2 : WIDE, cus, a.force_rows);
   const auto launch_up = [&](auto is_gated, auto nf) {
     constexpr int NF = decltype(nf)::value;
+    a.up_tiles = (int)grid(a.d_ff, NF, 1).x;
     moe_up_kernel<E, FP8, decltype(is_gated)::value, MF, NF>
         <<<grid(a.d_ff, NF, first_rows), 64 * waves_of(MF), 0, s>>>(a);
   };
@@ -936,6 +1146,11 @@ hipError_t launch_moe(const MoeCall& c, int cus, int force_rows, hipStream_t s) 
   a.h_lo = a.h_hi + (size_t)sh.tokens * sh.top_k * l.ldh;
   a.ldh = l.ldh;
   a.part = reinterpret_cast<float*>(ws + l.part);
+  if (sh.type == GEMM_TYPE_F16) {
+    a.h_wide = reinterpret_cast<float*>(ws + l.wide);
+    a.flags = reinterpret_cast<uint32_t*>(ws + l.flags);
+    a.peaks = reinterpret_cast<uint32_t*>(ws + l.peaks);
+  }
   const bool fp8 = sh.weight_type == GEMM_TYPE_E4M3, gated = sh.gated != 0;
   if (sh.type == GEMM_TYPE_F16)
     return fp8 ? launch_moe_as<LmF16, true>(a, gated, cus, s)
