@@ -176,6 +176,10 @@ int fp8_quantize(int rows, int cols, int type, const void* X, int ldx, int block
  * gemm_act_t, C of `type` F32, F16 or BF16, rounded once to nearest even.
  * Bytes of A and B past column K are not used.  alpha == 0 or K == 0: A, B and
  * the scales are not read.
+ * A block's two scales are multiplied with each other first, in fp32.  Where their
+ * product is below 2^-126 (as of a zero row's scale, 2^-126, with most others) the
+ * block's term, itself below 2^-101, is off by up to 2^-125; where it passes
+ * fp32's range the term is infinite, or NaN if the block's sum is 0.
  * fast_sums 0: each block's sum is formed in fp32 from exact products.
  * fast_sums 1: by the 8-bit matrix instructions, at twice the rate; they add
  * eight consecutive columns at a time and drop, of each product, what lies below
