@@ -308,8 +308,8 @@ int fp8_tile(const Fp8Call& c, int cus, int force) {
   const auto tiles = [&](int m, int n) {
     return (((int64_t)c.M + m - 1) / m) * (((int64_t)c.N + n - 1) / n);
   };
-  // 32-bit row and tile numbers in the tiled kernels.
-  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) &&
+  // 32-bit row, column and tile numbers in the tiled kernels.
+  const bool tiled = c.M <= (1 << 30) && c.N <= (1 << 30) && c.K <= (1 << 30) &&
                      tiles(64, 64) < (1 << 23);   // (fewer than 2^32 threads)
   const bool direct = fp8_direct(c), wide = c.fast_sums && c.b_rows == 128;
   static const int kSplit[6][2] = {{64, 32}, {64, 16}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
