@@ -19,7 +19,10 @@
 // blocks of 16-bit values; there x and s are first multiplied by 2^64, exactly.
 // For 16-bit inputs scale and quotient are fp32 numbers.  For fp32 inputs
 // they are formed in 64 bits and rounded once: rounded twice, one or two of 4096 x
-// 4096 weights went to the wrong side of the middle between two e4m3 numbers.
+// 4096 weights went to the wrong side of the middle between two e4m3 numbers.  And
+// they are the exact quotient's: 448 x / amax with neither factor rounded, since
+// values of few bits (16-bit ones held in fp32) meet such middles, and a rounded
+// amax / 448 sent 210 of 280000 pairs of them to the odd neighbour.
 // The 64-bit quotient reaches the conversion as an fp32 number whose last bit
 // stands for everything below it, so that nothing is lost before it.  16-bit
 // inputs would pay for that: 4096 x 14336 both ways 81 us against 57, bound by the
@@ -133,18 +136,20 @@ struct Scale {
 };
 template <>
 struct Scale<GEMM_TYPE_F32> {
+  // x / s as 7 x / (7 s): 448 = 7 x 64, so that both are exact in 64 bits.
+  static constexpr double kPart = 7.0;
   float s;
   double r, sc;
   __device__ __forceinline__ explicit Scale(float amax) {
-    double s64 = (double)amax * (1.0 / kE4m3Max);
-    if (s64 < kMinScale) s64 = kMinScale;
-    s = (float)s64;
-    r = 1.0 / s64;
-    sc = s64 <= 3.5e38 ? s64 : 0.0;
+    double s7 = (double)amax * (kPart / kE4m3Max);
+    if (s7 < kPart * kMinScale) s7 = kPart * kMinScale;
+    s = (float)(s7 * (1.0 / kPart));
+    r = 1.0 / s7;
+    sc = s7 <= 3.5e38 ? s7 : 0.0;
   }
   __device__ __forceinline__ float operator()(float x) const {
-    const double q0 = (double)x * r;
-    const double q = __builtin_fma(-__builtin_fma(q0, sc, -(double)x), r, q0);
+    const double x7 = kPart * (double)x, q0 = x7 * r;
+    const double q = __builtin_fma(-__builtin_fma(q0, sc, -x7), r, q0);
     const uint64_t bits = __builtin_bit_cast(uint64_t, q);
     const uint32_t lo = (uint32_t)bits, below = lo & 0x1fffffffu;   // what fp32 does not hold
     const uint32_t odd = (lo & 0xe0000000u) | (below != 0 ? 0x20000000u : 0u);

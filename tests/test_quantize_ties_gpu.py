@@ -56,3 +56,24 @@ def test_the_tie_of_the_header():
     x[0, :2] = torch.tensor([62.0, 2.90625])
     got, _ = run_quantize(x, 1, turned=False)
     assert got[0].view(E4M3).float()[0, :2].tolist() == [448.0, 22.0]
+
+
+@pytest.mark.parametrize("b", [1, 128])
+@pytest.mark.parametrize("type_", ["bf16", "f16"])
+def test_fp32_ties_go_to_even(type_, b):
+    """fp32 inputs are divided by the scale before it is rounded: the same pairs, held in fp32, are the
+    exact quotient's rounding everywhere."""
+    note("quantize fp32 pairs %s block %d" % (type_, b))
+    x = pairs(type_).float()
+    if b == 128:     # one row a block
+        x = torch.nn.functional.pad(x[::7, None], (0, 0, 0, 127)).reshape(-1, 128)
+    kept = slice(None) if b == 1 else slice(None, None, 128)
+    (got, s), turned = run_quantize(x, b)
+    assert torch.equal(s, reference(x, b)[1])
+    want = ideal(x[kept]).float()
+    assert torch.equal(got[kept].view(E4M3).float(), want)
+    if b == 128:     # (along columns the blocks of 1 x 128 are others)
+        assert torch.equal(turned[0].t()[kept].contiguous().view(E4M3).float(), want)
+    else:
+        (_, other) = run_quantize(x.t().contiguous(), 1)
+        assert torch.equal(other[0].view(E4M3).float(), want)
