@@ -298,12 +298,13 @@ hipError_t launch_ksplit(const Fp8Call& c, hipStream_t s) {
 //    1.53, then 0.70 and 2.10; more tiles than two per CU in proportion;
 //  * K-split tiles of m x n take (m + n) K bytes through a CU's load path at 23
 //    bytes a nanosecond.
-// So 24 x 4096 x 4096 runs 32 x 16 K-split tiles (9.4 us; 64 x 64: 15.5), 64 x
-// 14336 x 4096 the 64 x 64 ones (13; K-split 31), 4096 x 14336 x 4096 128 x 256 (230;
-// 128 x 128: 245).  Through registers a tile takes about twice its time.  Of the 64 x
+// So 24 x 4096 x 4096 runs 32 x 16 K-split tiles (8.3 us a pass; 64 x 64: 11.6), 64 x
+// 14336 x 4096 the 64 x 64 ones (13.3; K-split 31), 4096 x 14336 x 4096 128 x 256 (254;
+// 128 x 128: 301).  Through registers a tile counts as twice its time (measured 2.3
+// times in 1000 x 3000 x 777, 4.3 in 4096 x 14336 x 4096).  Of the 64 x
 // 64 tiles the one with three stages lets three workgroups share a CU, which
 // pays where all run at once that way and not with two (1000 x 3000 x 777, 752 tiles:
-// 10.9 against 12.8; 512 x 4096 x 4096, 512 tiles: 18.3 against 17.3).
+// 10.6 against 12.8; 512 x 4096 x 4096, 512 tiles: 16.9 against 17.1).
 int fp8_tile(const Fp8Call& c, int cus, int force) {
   const auto tiles = [&](int m, int n) {
     return (((int64_t)c.M + m - 1) / m) * (((int64_t)c.N + n - 1) / n);

@@ -22,9 +22,9 @@
 // second product; the sum over a token's slots.  For one token the last two are one.
 //
 // Measured (us of kernel time; the card reads 6.2 TB/s): 64 tokens, 8 experts of 4096
-// x 14336 in bfloat16: 345 (5.5 TB/s) and 197 (4.8); 4 tokens, 64 experts of 4096 x
-// 1536 in e4m3: 72 (4.6) and 41 (4.1), logits 4.9, sum 4.7; one token, 8 experts
-// of 1024 x 512: 2.5, 6.8 and 4.7, latency throughout.
+// x 14336 in bfloat16: 345 (5.5 TB/s) and 196 (5.1); 4 tokens, 64 experts of 4096 x
+// 1536 in e4m3: 69 (5.0) and 39 (4.4), logits 4.8, sum 4.7; one token, 8 experts
+// of 1024 x 512: 2.4, 6.7 and 4.7, latency throughout.  (Rates from counted bytes.)
 //
 // The logits are summed in 64 bits: two experts' logits can lie closer than
 // fp32 sums of a few thousand terms resolve, and the choice between them is an

@@ -196,7 +196,7 @@ __device__ __forceinline__ void store8_upto(uint8_t* p, u32x2 v, int valid) {
 // One scale per row and block of 128 columns, no transpose: 16 lanes take one
 // such block, eight columns each, and a wave 16 rows of one block of columns.
 // Bound by memory; with few rows by the latency of one load, a wave reduction
-// and one store (8 x 4096 bfloat16: 3.0 us, the time of an empty launch and a load).
+// and one store (8 x 4096 bfloat16: 3.1 us, the time of an empty launch and a load).
 template <int TYPE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeCall p) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeCall p) {
 // (slot g of column j of chunk c lies at g ^ c, which spreads the writes over
 // the banks) and leaves in whole 128-byte rows.
 // Bound by memory: 4096 x 14336 bfloat16 both ways 57 us (4.1 TB/s, a copy reaches
-// 5.1), 4096 x 4096 fp32 in 128 x 128 blocks both ways 18.5 (5.4).
+// 5.1; the vector unit is busy 59 %), 4096 x 4096 fp32 in 128 x 128 blocks both ways
+// 18.5 to 20 (5.0 and more).
 // PLAIN / TURNED: which of the two are wanted; BLOCK: one scale per 128 x 128.
 template <int TYPE, bool PLAIN, bool TURNED, bool BLOCK>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantizeCall p) {
