@@ -1035,8 +1035,18 @@ __global__ void __launch_bounds__(512) moe_down_token_kernel(MoeArgs p) {
   join(total, part, wave, lane);
   if (threadIdx.x < 16 && n0 + (int)threadIdx.x < D) {
     const int at = 64 * (threadIdx.x / 4) + threadIdx.x % 4;   // (column 0 of the result: the token)
-    p.Y[n0 + threadIdx.x] =
-        E::bits(joined(part, 0, at));
+    float y = joined(part, 0, at);
+    if constexpr (E::kNarrow && !FP8) {
+      if (y != y) {   // (an infinite weight may have met an hi of zero: see high_sum)
+        y = 0.0f;
+        for (int s = 0; s < p.top_k; ++s) {
+          const uint16_t* w_at = static_cast<const uint16_t*>(p.W2) +
+                                 ((int64_t)p.ids[s] * D + n0 + threadIdx.x) * p.ld2;
+          y = __builtin_fmaf(p.w[s], high_sum<E>(w_at, p.h_wide + s * p.ldh, I), y);
+        }
+      }
+    }
+    p.Y[n0 + threadIdx.x] = E::bits(y);
   }
 }
 

@@ -156,3 +156,27 @@ def test_small_rows_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(m.y, want)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 4, 3), (3, 1, 1), (40, 4, 2)])
+def test_infinite_weight_of_a_value_that_rounds_to_zero(T, E, k):
+    """h of one column is below 2^-25 in a row of ordinary size: its product with an infinite weight is
+    infinite all the same."""
+    m = Layer(T, 77, 45, E, k, "f16", gated=False, act=lib.ACT_NONE, seed=57, size=1.0)
+    m.x = (m.x.abs().float() * 2.0 ** -8).half()
+    m.w1 = [w.clone() for w in m.w1]
+    for w in m.w1:
+        w[40] = -(2.0 ** -24)
+    m.d1[:, 40, :77] = -(2.0 ** -24)
+    m.buffers()
+    m.call()
+    torch.cuda.synchronize()
+    clean = m.y[:, :77].clone()
+    assert clean.isfinite().all()
+    m.d2[:, 9, 40] = float("-inf")
+    m.call()
+    torch.cuda.synchronize()
+    got = m.y[:, :77]
+    assert (got[:, 9] == float("inf")).all()
+    got[:, 9] = clean[:, 9]
+    assert torch.equal(got, clean)
