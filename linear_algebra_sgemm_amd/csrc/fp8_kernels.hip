@@ -303,8 +303,9 @@ hipError_t launch_ksplit(const Fp8Call& c, hipStream_t s) {
 // 128 x 128: 301).  Through registers a tile counts as twice its time (measured 2.3
 // times in 1000 x 3000 x 777, 4.3 in 4096 x 14336 x 4096).  Of the 64 x
 // 64 tiles the one with three stages lets three workgroups share a CU, which
-// pays where all run at once that way and not with two (1000 x 3000 x 777, 752 tiles:
-// 10.6 against 12.8; 512 x 4096 x 4096, 512 tiles: 16.9 against 17.1).
+// pays where all run at once that way and not with two: 576 to 768 tiles of N = 4096
+// and K = 768, 2048 and 4096 9 to 20 % (640 x 4096 x 2048: 13.8 against 16.4); 512 tiles
+// the same (10.5, 10.3), 832 and 1024 up to 5 % slower (19.0, 18.3).
 int fp8_tile(const Fp8Call& c, int cus, int force) {
   const auto tiles = [&](int m, int n) {
     return (((int64_t)c.M + m - 1) / m) * (((int64_t)c.N + n - 1) / n);
