@@ -150,10 +150,10 @@ int bgemm_bias_act(int M, int N, int K, float alpha,
  * F32, F16 or BF16; the last blocks of a row or column may be shorter),
  *   Q[i][j] = x[i][j] / s, rounded to e4m3 to nearest even,
  *   S[j / 128][i] = s  (block_rows 1)  or  S[j / 128][i / 128] = s  (128),
- * s and x / s rounded to fp32 for 16-bit X, for FP32 X the quotient by an s that is
- * not rounded (with a rounded s a quotient that is a tie in exact arithmetic may miss the middle and
- * go to either neighbour: a bfloat16 x = 2.90625 in a block with max|x| = 62 gives
- * 22, where 448 x / 62 is 21, a tie that even takes to 20),
+ * s and x / s rounded to fp32 for 16-bit X; for FP32 X the quotient is by s before
+ * it is rounded.  (A quotient that is a tie in exact arithmetic may go to either
+ * neighbour with a rounded s: a bfloat16 x = 2.90625 in a block with max|x| = 62
+ * gives 22, where 448 x / 62 is 21, a tie that even takes to 20.)
  * Q rows x cols with leading dimension ldq >= cols, S with lds >= rows, or >=
  * ceil(rows / 128).  QT, ST: the same of the transpose of X: QT cols x rows
  * (ldqt >= rows), blocks of 128 rows of X by one column (ST[i / 128][j]) or by
