@@ -20,7 +20,7 @@
 // while the other meets at its barrier or writes its results (a 256 x 256 tile of eight
 // waves took 313 us); counted over the whole launch the vector unit is busy 54 % and
 // the matrix unit 45 % of the time, waves wait 24 %, so neither alone is the bound.
-// Measured, a pass among others: 4096 x 14336 x 4096 with GELU 256 us (1880 TFLOP/s; a
+// Measured, a pass among others, on the fastest of several cards (the slowest 5 % more): 4096 x 14336 x 4096 with GELU 256 us (1880 TFLOP/s; a
 // plain 8-bit library product with one scale 185), the same with a scale for every row
 // of B 331 (1450), with fp32 sums 456 to 468 (1030), with rows off 16-byte
 // boundaries 1110 (433); 4096 x 4096 x 8192 with fp32 sums and a scale for every row of
