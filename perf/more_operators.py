@@ -1,0 +1,430 @@
+"""The 8-bit integer path of an expert layer with many tokens, as measured: rows quantised to int8, the
+product with a scale for every token and channel, the same product of tokens grouped by expert, and the
+exchange of tokens with the experts' order, back, and backward.
+
+Every case has a plain form (elementary torch operations in 32 bits) and the framework's call; `own`
+chooses between them.  Weights are N x K, one channel a row, so that tokens and channels are quantised
+alike: Q[r] = X[r] / S[r], S[r] = max|X[r]| / 127.
+"""
+import math
+
+import torch
+
+own = False
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+SMALLEST = 2.0 ** -126
+
+
+# ---------------------------------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # One decoding step's activations before an 8-bit product: all latency.
+        {"name": "rows_decode", "op": "rows", "rows": 8, "cols": 4096, "type": "bf16"},
+        # The inner activations of a feed-forward layer over a prompt.
+        {"name": "rows_prompt", "op": "rows", "rows": 4096, "cols": 14336, "type": "bf16"},
+        # One token through a square projection: the weight's bytes are everything.
+        {"name": "product_token", "op": "product", "M": 1, "N": 4096, "K": 4096, "out": "bf16",
+         "bias": False, "act": 0, "gated": False, "pad": 0},
+        # A serving batch through a gated up projection: twice the weight, half the result.
+        {"name": "product_batch", "op": "product", "M": 64, "N": 14336, "K": 4096, "out": "bf16",
+         "bias": False, "act": 2, "gated": True, "pad": 0},
+        # The framework's feed-forward workload: 4096 tokens, bias and GELU.
+        {"name": "product_ffn", "op": "product", "M": 4096, "N": 14336, "K": 4096, "out": "f16",
+         "bias": True, "act": 1, "gated": False, "pad": 0},
+        # The framework's ragged shape: no size a multiple of a tile, rows padded to 16 bytes.
+        {"name": "product_ragged", "op": "product", "M": 1000, "N": 3000, "K": 777, "out": "f32",
+         "bias": True, "act": 0, "gated": False, "pad": 7},
+        # Four sequences decoding: a few rows for each of some of the experts.
+        {"name": "grouped_decode", "op": "grouped", "T": 4, "D": 4096, "N": 1024, "E": 64, "k": 8,
+         "out": "bf16", "act": 2, "gated": True, "gather": True, "lost": 0.0, "skew": 0.0, "pad": 0},
+        # A prompt through the up projection of every expert, tokens read where they lie; some experts
+        # are more popular than others.
+        {"name": "grouped_prompt", "op": "grouped", "T": 2048, "D": 4096, "N": 1024, "E": 64, "k": 8,
+         "out": "bf16", "act": 2, "gated": True, "gather": True, "lost": 0.0, "skew": 0.5, "pad": 0},
+        # Sixteen sequences' tokens put into the experts' order: launches and latency.
+        {"name": "dispatch_decode", "op": "dispatch", "T": 16, "D": 4096, "E": 64, "k": 8,
+         "type": "bf16", "weighted": False, "lost": 0.0, "skew": 0.0},
+        # A training batch's, an eighth of it padding: the copies' bytes.
+        {"name": "dispatch_train", "op": "dispatch", "T": 4096, "D": 4096, "E": 64, "k": 8,
+         "type": "bf16", "weighted": False, "lost": 0.125, "skew": 0.5},
+        # Back into the tokens' order, with the router's weights.
+        {"name": "combine_prompt", "op": "combine", "T": 4096, "D": 4096, "E": 64, "k": 8,
+         "type": "bf16", "weighted": True, "grad": False, "lost": 0.0, "skew": 0.5},
+        # That step's gradients, for the experts' results and for the weights, odd sizes.
+        {"name": "combine_grad", "op": "combine", "T": 3001, "D": 2050, "E": 60, "k": 6,
+         "type": "f16", "weighted": True, "grad": True, "lost": 0.0, "skew": 0.5},
+    ]
+
+
+def _size(rng, low, high, multiple=1):
+    """Spread over the logarithm; mostly whole multiples, one in four as it falls."""
+    n = int(round(math.exp(rng.uniform(math.log(low), math.log(high)))))
+    if multiple > 1 and rng.random() < 0.75:
+        n = max(multiple, n // multiple * multiple)
+    return min(max(n, low), high)
+
+
+MOST = 4096 * 14336 * 4096
+
+
+def _routing(rng, tokens):
+    case = {"T": _size(rng, 1, tokens), "D": _size(rng, 512, 8192, 64),
+            "E": rng.choice([4, 8, 16, 32, 60, 64, 128]), "k": 0,
+            "lost": rng.choice([0.0, 0.0, 0.125]), "skew": rng.choice([0.0, 0.5])}
+    case["k"] = rng.choice([k for k in (1, 2, 4, 6, 8) if k <= case["E"]])
+    return case
+
+
+def draw(rng):
+    op = rng.choice(["rows", "product", "product", "grouped", "grouped", "dispatch", "combine"])
+    if op == "rows":
+        while True:
+            case = {"op": op, "rows": _size(rng, 1, 16384, 8), "cols": _size(rng, 64, 16384, 64),
+                    "type": rng.choice(["bf16", "f16", "f32"])}
+            if case["rows"] * case["cols"] <= 4096 * 14336:
+                return case
+    if op == "product":
+        while True:
+            case = {"op": op, "M": _size(rng, 1, 8192, 16), "N": _size(rng, 64, 16384, 64),
+                    "K": _size(rng, 64, 16384, 64), "out": rng.choice(["bf16", "f16", "f32"]),
+                    "bias": rng.random() < 0.5, "act": rng.choice([0, 0, 1, 2]),
+                    "gated": rng.random() < 0.25, "pad": 0}
+            case["pad"] = -case["K"] % 16 if rng.random() < 0.75 else 0
+            if case["M"] * case["N"] * case["K"] * (1 + case["gated"]) <= MOST:
+                return case
+    if op == "grouped":
+        while True:
+            case = {"op": op, **_routing(rng, 4096), "N": _size(rng, 256, 8192, 64),
+                    "out": rng.choice(["bf16", "f16", "f32"]), "act": rng.choice([0, 1, 2]),
+                    "gated": rng.random() < 0.5, "gather": rng.random() < 0.5, "pad": 0}
+            case["pad"] = -case["D"] % 16 if rng.random() < 0.75 else 0
+            weights = case["E"] * case["D"] * case["N"] * (1 + case["gated"])
+            if (case["T"] * case["k"] * weights // case["E"] <= MOST // 4
+                    and weights <= 64 * 4096 * 2048):
+                return case
+    while True:
+        case = {"op": op, **_routing(rng, 16384), "type": rng.choice(["bf16", "f16", "f32"]),
+                "weighted": rng.random() < (0.25 if op == "dispatch" else 0.75)}
+        if op == "combine":
+            case["grad"] = rng.random() < 0.5
+        if case["T"] * case["k"] * case["D"] * (2 if case["type"] == "f32" else 1) <= 2 ** 26:
+            return case
+
+
+# --------------------------------------------------------------------------------------- inputs
+
+def _ld(cols, pad):
+    """`pad` 0: rows as they fall; else rows padded to whole 16-element steps."""
+    return cols if not pad else -(-cols // 16) * 16
+
+
+def _generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(g, shape, spread=1.0):
+    return torch.randn(shape, generator=g, device="cuda", dtype=torch.float32).mul_(spread)
+
+
+def _as_int8(x):
+    """Rows of x (..., rows, cols) as whole numbers of -127 .. 127 and a scale for each row."""
+    s = x.abs().amax(dim=-1)
+    s = (s / torch.full_like(s, 127.0)).clamp_min_(SMALLEST)
+    return torch.round(x / s[..., None]).to(torch.int8), s
+
+
+def _weights(g, experts, rows, cols, ld):
+    """A stack of quantised weights in rows of ld, the rest of each row what must never count."""
+    q = torch.full((experts, rows, ld), -128, device="cuda", dtype=torch.int8)
+    s = torch.empty((experts, rows), device="cuda")
+    step = max(1, 2 ** 28 // (rows * cols))
+    for e in range(0, experts, step):
+        n = min(step, experts - e)
+        q[e:e + n, :, :cols], s[e:e + n] = _as_int8(_normal(g, (n, rows, cols), 0.02))
+    return q, s
+
+
+def _experts(g, case):
+    """The experts that every token chose (the k largest of its logits), -1 for tokens of the padding."""
+    T, E, k = case["T"], case["E"], case["k"]
+    logits = _normal(g, (T, E)) + case["skew"] * _normal(g, (1, E))
+    p, ids = torch.softmax(logits, 1).topk(k, dim=1)
+    out = torch.rand((T, 1), generator=g, device="cuda") < case["lost"]
+    return ids.masked_fill(out, -1).int(), p.masked_fill(out, 0.0)
+
+
+def _sorted(ids, experts):
+    """Rows in the experts' order: where each expert's begin, the (token, slot) of every row, -1 behind
+    the last, and the row of every (token, slot), -1 for those of no expert."""
+    flat = ids.flatten().long()
+    key = torch.where((flat >= 0) & (flat < experts), flat, experts)
+    count = (key[None] == torch.arange(experts, device=key.device)[:, None]).sum(1)
+    offsets = torch.cat([count.new_zeros(1), count.cumsum(0)])
+    order = torch.sort(key, stable=True).indices
+    row = torch.empty_like(order)
+    row[order] = torch.arange(len(order), device=order.device)
+    src = torch.where(torch.arange(len(order), device=order.device) < offsets[-1], order, -1)
+    return offsets.int(), src.int(), torch.where(key < experts, row, -1).int().view(ids.shape)
+
+
+def prepare(case, seed):
+    g = _generator(seed)
+    s = dict(case)
+    if case["op"] == "rows":
+        rows, cols = case["rows"], case["cols"]
+        # Activations: rows and channels of unequal size, a few channels far larger than the rest.
+        x = _normal(g, (rows, cols))
+        x *= torch.exp(_normal(g, (rows, 1)))
+        x *= 1 + 30 * (torch.rand((1, cols), generator=g, device="cuda") < 0.003)
+        s["X"] = x.to(TYPES[case["type"]])
+        s["Q"] = torch.empty((rows, cols), device="cuda", dtype=torch.int8)
+        s["S"] = torch.empty(rows, device="cuda")
+        return s
+    if case["op"] == "product":
+        M, N, K = case["M"], case["N"], case["K"]
+        wide = N * (1 + case["gated"])
+        s["ld"] = _ld(K, case["pad"])
+        a, s["SA"] = _as_int8(_normal(g, (M, K)))
+        s["A"] = torch.full((M, s["ld"]), -128, device="cuda", dtype=torch.int8)
+        s["A"][:, :K] = a
+        b, sb = _weights(g, 1, wide, K, s["ld"])
+        s["B"], s["SB"] = b[0], sb[0]
+        s["bias_v"] = _normal(g, (wide,)) if case["bias"] else None
+        s["C"] = torch.empty((M, N), device="cuda", dtype=TYPES[case["out"]])
+        return s
+    T, D, E, k = (case[n] for n in ("T", "D", "E", "k"))
+    s["ids"], s["w"] = _experts(g, case)
+    if case["op"] == "dispatch":
+        s["X"] = _normal(g, (T, D)).to(TYPES[case["type"]])
+        for name, n in (("offsets", E + 1), ("src", T * k), ("pos", T * k)):
+            s[name] = torch.empty(n, device="cuda", dtype=torch.int32)
+        s["Y"] = torch.zeros((T * k, D), device="cuda", dtype=TYPES[case["type"]])
+        return s
+    s["offsets"], s["src"], s["pos"] = _sorted(s["ids"], E)
+    if case["op"] == "grouped":
+        s["ld"] = _ld(D, case["pad"])
+        rows = T if case["gather"] else T * k
+        a, s["SA"] = _as_int8(_normal(g, (rows, D)))
+        s["A"] = torch.full((rows, s["ld"]), -128, device="cuda", dtype=torch.int8)
+        s["A"][:, :D] = a
+        s["B"], s["SB"] = _weights(g, E, case["N"] * (1 + case["gated"]), D, s["ld"])
+        s["C"] = torch.zeros((T * k, case["N"]), device="cuda", dtype=TYPES[case["out"]])
+        return s
+    s["X"] = _normal(g, (T * k, D)).to(TYPES[case["type"]])
+    if case["grad"]:
+        s["dY"] = _normal(g, (T, D)).to(TYPES[case["type"]])
+        s["dX"] = torch.zeros_like(s["X"])
+        s["dw"] = torch.empty((T, k), device="cuda")
+    else:
+        s["Y"] = torch.empty((T, D), device="cuda", dtype=TYPES[case["type"]])
+    return s
+
+
+# ----------------------------------------------------------------------------- the framework's calls
+
+_handle = None
+
+
+def _library():
+    """The package, its library created once, as a program does at its start."""
+    global _handle
+    if _handle is None:
+        import linear_algebra_sgemm_amd as lib
+        lib.gemm_create()
+        _handle = lib
+    return _handle
+
+
+def _run_own(s):
+    lib = _library()
+    types = {"f32": lib.TYPE_F32, "f16": lib.TYPE_F16, "bf16": lib.TYPE_BF16}
+    if s["op"] == "rows":
+        lib.i8_quantize(s["rows"], s["cols"], types[s["type"]], s["X"], s["cols"], s["Q"], s["cols"],
+                        s["S"])
+        return [s["Q"], s["S"]]
+    if s["op"] == "product":
+        lib.i8_gemm_bias_act(s["M"], s["N"], s["K"], 1.0, s["A"], s["ld"], s["SA"], s["B"], s["ld"],
+                             s["SB"], s["bias_v"], s["act"], s["gated"], types[s["out"]], s["C"],
+                             s["N"])
+        return [s["C"]]
+    T, D, E, k = (s[n] for n in ("T", "D", "E", "k"))
+    if s["op"] == "grouped":
+        index, per = (s["src"], k) if s["gather"] else (None, 1)
+        lib.i8_gemm_grouped(E, s["offsets"], T * k, s["N"], D, 1.0, s["A"], s["ld"], s["SA"],
+                            s["A"].shape[0], index, per, s["B"], s["ld"], s["SB"], None, s["act"],
+                            s["gated"], types[s["out"]], s["C"], s["N"])
+        return [s["C"]]
+    if s["op"] == "dispatch":
+        if "ws" not in s:   # kept with the buffers, as a program keeps it
+            s["ws"] = torch.empty(lib.moe_sort_workspace(T, k, E), device="cuda", dtype=torch.uint8)
+        lib.moe_sort(T, k, E, s["ids"], s["offsets"], s["src"], s["pos"], s["ws"], s["ws"].numel())
+        lib.moe_gather(T * k, D, types[s["type"]], s["X"], D, T, s["src"], k,
+                       s["w"] if s["weighted"] else None, s["Y"], D)
+        return [s["offsets"], s["src"], s["pos"], s["Y"]]
+    w = s["w"] if s["weighted"] else None
+    if s["grad"]:
+        lib.moe_combine_grad(T, k, D, types[s["type"]], s["dY"], D, s["X"], D, T * k, s["pos"], w,
+                             s["dX"], D, s["dw"])
+        return [s["dX"], s["dw"]]
+    lib.moe_combine(T, k, D, types[s["type"]], s["X"], D, T * k, s["pos"], w, s["Y"], D)
+    return [s["Y"]]
+
+
+# -------------------------------------------------------------------------------------- plain form
+
+def _act(x, act):
+    if act == 1:
+        return 0.5 * x * (1 + torch.tanh(math.sqrt(2 / math.pi) * (x + 0.044715 * x * x * x)))
+    return x * torch.sigmoid(x) if act == 2 else x
+
+
+def _finish(u, n, case):
+    u = _act(u[..., :n], case["act"]) * u[..., n:] if case["gated"] else _act(u, case["act"])
+    return u.to(TYPES[case["out"]])
+
+
+def _run_plain(s):
+    if s["op"] == "rows":
+        return list(_as_int8(s["X"].float()))
+    if s["op"] == "product":
+        u = s["A"][:, :s["K"]].float() @ s["B"][:, :s["K"]].float().t()
+        u = u * s["SA"][:, None] * s["SB"]
+        if s["bias"]:
+            u = u + s["bias_v"]
+        return [_finish(u, s["N"], s)]
+    T, D, E, k = (s[n] for n in ("T", "D", "E", "k"))
+    if s["op"] == "grouped":
+        # Every used expert's rows side by side, as many as the fullest has: one batched product.
+        offsets = s["offsets"].long()
+        count = offsets[1:] - offsets[:-1]
+        used = torch.nonzero(count)[:, 0]
+        place = torch.arange(int(count.max()), device="cuda")
+        here = place < count[used, None]
+        row = torch.where(here, offsets[used, None] + place, 0)
+        read = s["src"].long()[row] // k if s["gather"] else row
+        read = torch.where(here, read, 0)
+        u = s["A"][:, :D][read].float() @ s["B"][..., :D][used].float().transpose(1, 2)
+        u = u * s["SA"][read][..., None] * s["SB"][used][:, None]
+        c = torch.zeros_like(s["C"])
+        c[row[here]] = _finish(u, s["N"], s)[here]
+        return [c]
+    if s["op"] == "dispatch":
+        offsets, src, pos = _sorted(s["ids"], E)
+        at = src.long().clamp_min(0)
+        y = s["X"].float()[at // k]
+        if s["weighted"]:
+            y = y * s["w"].flatten()[at][:, None]
+        y = torch.where((src >= 0)[:, None], y, 0.0)
+        return [offsets, src, pos.flatten(), y.to(s["X"].dtype)]
+    valid = s["pos"] >= 0
+    at = s["pos"].long().clamp_min(0)
+    w = torch.where(valid, s["w"] if s["weighted"] else 1.0, 0.0)
+    x = s["X"].float()[at]
+    if not s["grad"]:
+        return [(x * w[..., None]).sum(1).to(s["X"].dtype)]
+    dy = s["dY"].float()[:, None]
+    dw = torch.where(valid, (x * dy).sum(2), 0.0)
+    dx = torch.zeros_like(s["X"])
+    dx[at[valid]] = (w[..., None] * dy).to(dx.dtype)[valid]
+    return [dx, dw]
+
+
+def run(state):
+    return _run_own(state) if own else _run_plain(state)
+
+
+# --------------------------------------------------------------------------- what a pass cannot avoid
+
+def work(case):
+    wide = {"f32": 4, "f16": 2, "bf16": 2}
+    if case["op"] == "rows":
+        n = case["rows"] * case["cols"]
+        return {"bytes": n * (wide[case["type"]] + 1) + 4 * case["rows"], "flops": 2 * n}
+    if case["op"] == "product":
+        M, N, K, both = (case[n] for n in ("M", "N", "K", "gated"))
+        rows = N * (1 + both)
+        return {"bytes": (M + rows) * K + wide[case["out"]] * M * N + 4 * (M + rows)
+                + (4 * rows if case["bias"] else 0), "flops": 2 * M * rows * K}
+    T, D, E, k = (case[n] for n in ("T", "D", "E", "k"))
+    live = T * (1 - case["lost"])
+    if case["op"] == "grouped":
+        rows = case["N"] * (1 + case["gated"])
+        # Experts that tokens choose evenly at random leave some unread.
+        used = E * (1 - (1 - k / E) ** live)
+        read = live if case["gather"] else live * k
+        return {"bytes": int(used * rows * (D + 4) + read * (D + 4)
+                             + live * k * (case["N"] * wide[case["out"]] + 4)),
+                "flops": int(2 * live * k * rows * D)}
+    row = D * wide[case["type"]]
+    if case["op"] == "dispatch":
+        return {"bytes": int(live * row + live * k * row + T * k * 12 + 4 * E), "flops": T * k * E}
+    if case["grad"]:
+        return {"bytes": int(T * row + 2 * live * k * row + T * k * 12), "flops": int(3 * live * k * D)}
+    return {"bytes": int(T * row + live * k * row + T * k * 8), "flops": int(2 * live * k * D)}
+
+
+# ------------------------------------------------------------------------------ the definition, 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "rows":
+        # (The whole numbers follow the scale as it is held: they have to be equal, not near.)
+        return [None, torch.clamp(s["X"].double().abs().max(1).values / 127, min=2.0 ** -126)]
+    if case["op"] == "product":
+        a = s["A"][:, :case["K"]].double().mul_(s["SA"].double()[:, None])
+        b = s["B"][:, :case["K"]].double().mul_(s["SB"].double()[:, None])
+        c = torch.mm(a, b.t())
+        if case["bias"]:
+            c.add_(s["bias_v"].double())
+        return [_curve(c, case)]
+    T, D, E, k = (case[n] for n in ("T", "D", "E", "k"))
+    ids, x = s["ids"].flatten(), s.get("X")
+    if case["op"] == "grouped":
+        c = torch.zeros(s["C"].shape, dtype=torch.float64, device="cuda")
+        begin = 0
+        for e in range(E):
+            chose = torch.nonzero(ids == e)[:, 0]
+            rows = torch.arange(begin, begin + len(chose), device="cuda")
+            begin += len(chose)
+            read = torch.div(chose, k, rounding_mode="floor") if case["gather"] else rows
+            a = s["A"][read, :D].double().mul_(s["SA"][read].double()[:, None])
+            b = s["B"][e, :, :D].double().mul_(s["SB"][e].double()[:, None])
+            c[rows] = _curve(torch.mm(a, b.t()), case)
+        return [c]
+    # The row of every (token, slot), expert by expert.
+    rows = torch.full((T * k,), -1, dtype=torch.int64, device="cuda")
+    begin = 0
+    for e in range(E):
+        chose = torch.nonzero(ids == e)[:, 0]
+        rows[chose] = torch.arange(begin, begin + len(chose), device="cuda")
+        begin += len(chose)
+    live = torch.nonzero(rows >= 0)[:, 0]
+    token = torch.div(live, k, rounding_mode="floor")
+    w = s["w"].flatten().double()[live] if case["weighted"] else torch.ones(len(live), device="cuda").double()
+    if case["op"] == "dispatch":
+        y = torch.zeros(s["Y"].shape, dtype=torch.float64, device="cuda")
+        y[rows[live]] = x.double()[token] * w[:, None]
+        return [None, None, None, y]
+    if not case["grad"]:
+        y = torch.zeros((T, D), dtype=torch.float64, device="cuda")
+        return [y.index_add_(0, token, x[rows[live]].double() * w[:, None])]
+    dx, dw = torch.zeros_like(x, dtype=torch.float64), torch.zeros(T * k, dtype=torch.float64, device="cuda")
+    dy = s["dY"].double()[token]
+    dx[rows[live]] = dy * w[:, None]
+    dw[live] = torch.linalg.vecdot(dy, x[rows[live]].double())
+    return [dx, dw.view(T, k)]
+
+
+def _curve(u, case):
+    """The activations from their definitions: GELU in its tanh form, x / (1 + e^-x); the gate."""
+    x = u[..., :case["N"]]
+    if case["act"] == 1:
+        v = 0.7978845608028653559 * (x + 0.044715 * x ** 3)
+        x = x / 2 + x / 2 * torch.tanh(v)
+    elif case["act"] == 2:
+        x = x / (1 + torch.exp(-x))
+    return x * u[..., case["N"]:] if case["gated"] else x
