@@ -262,8 +262,8 @@ def _run_own(s):
         if "ws" not in s:   # kept with the buffers, as a program keeps it
             s["ws"] = torch.empty(lib.moe_sort_workspace(T, k, E), device="cuda", dtype=torch.uint8)
         lib.moe_sort(T, k, E, s["ids"], s["offsets"], s["src"], s["pos"], s["ws"], s["ws"].numel())
-        lib.moe_gather(T * k, D, types[s["type"]], s["X"], D, T, s["src"], k,
-                       s["w"] if s["weighted"] else None, s["Y"], D)
+        lib.moe_dispatch(T, k, D, types[s["type"]], s["X"], D, s["pos"],
+                         s["w"] if s["weighted"] else None, s["Y"], D, T * k)
         return [s["offsets"], s["src"], s["pos"], s["Y"]]
     w = s["w"] if s["weighted"] else None
     if s["grad"]:
