@@ -58,10 +58,10 @@ typedef enum {
 typedef enum {
   GEMM_ACT_NONE = 0,      /* identity */
   GEMM_ACT_GELU_TANH = 1, /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
-  GEMM_ACT_SILU = 2       /* x / (1 + exp(-x)): the 8-bit product and moe_ffn only */
+  GEMM_ACT_SILU = 2       /* x / (1 + exp(-x)): the 8-bit products and moe_ffn only */
 } gemm_act_t;
 
-/* Element types of the 8-bit operators and moe_ffn.  E4M3 is the 8-bit format
+/* Element types of the 8-bit operators and the moe_ calls.  E4M3 is the 8-bit format
  * of 4 exponent and 3 mantissa bits with a NaN (bit patterns 0x7f, 0xff), no
  * infinity and the largest value 448. */
 typedef enum {
@@ -236,6 +236,105 @@ int moe_ffn(const moe_shape_t* shape, const uint16_t* X, int ldx, const uint16_t
             const void* W1, int ld1, const float* S1, const void* W2, int ld2, const float* S2,
             int* ids, float* w, uint16_t* Y, int ldy, void* workspace, size_t workspace_bytes,
             hipStream_t stream);
+
+/*
+ * Quantisation of rows to int8: with s = max(max|x| / 127, 2^-126) over row r of X
+ * (rows x cols, `type` F32, F16 or BF16, cols at most 2^20),
+ *   Q[r][j] = x[r][j] / s, rounded to the nearest whole number, ties to even,
+ *   S[r] = s,
+ * s and x / s rounded to fp32.  Tokens and the channels of a weight (one a row) are
+ * quantised alike.  Q rows x cols with ldq >= cols; S dense.  A row that holds a NaN or an
+ * infinity has that for its scale and zeros for its values, so that its products
+ * are NaN.  rows == 0 or cols == 0: nothing is done.
+ */
+int i8_quantize(int rows, int cols, int type, const void* X, int ldx,
+                int8_t* Q, int ldq, float* S, hipStream_t stream);
+
+/*
+ * The int8 product with a scale for every token and channel,
+ *   u[m][n] = alpha SA[m] SB[n] sum_k A[m][k] B[n][k] + bias[n],
+ *   C[m][n] = act(u[m][n]),  or with gated 1  act(u[m][n]) u[m][N + n],
+ * A M x K (lda >= K), B N x K, with a gate 2 N x K (ldb >= K; one channel a row, as
+ * i8_quantize lays it out), SA of length M, SB and bias (FP32, NULL = none) one value for
+ * every row of B, `act` of gemm_act_t, C (ldc >= N) of `type` F32, F16 or BF16, rounded
+ * once to nearest even.  K is at most 131071: the sums are exact, in int32, and are
+ * rounded to fp32 once before they are scaled.  All values of int8 may occur, -128
+ * too.  Bytes of A and B past column K are not used.  alpha == 0 or K == 0: A, B and the
+ * scales are not read.  With a gate N is at most 2^30.
+ */
+int i8_gemm_bias_act(int M, int N, int K, float alpha,
+                     const int8_t* A, int lda, const float* SA,
+                     const int8_t* B, int ldb, const float* SB,
+                     const float* bias, int act, int gated, int type, void* C, int ldc,
+                     hipStream_t stream);
+
+/*
+ * The same product of `groups` (at most 1024) sets of rows, each with a matrix of its own, as
+ * the experts of a layer take their tokens.  Row r, offsets[g] <= r < offsets[g + 1] (device
+ * memory, groups + 1 int32 numbers that ascend, as moe_sort writes them; the rows
+ * number at most M), is multiplied by group g's matrix: B, SB and bias hold the groups' one
+ * behind the other (N rows each, 2 N with a gate).  Rows outside every group are
+ * left as they were in C (M rows of it).
+ * `index` NULL: row r of the product is row r of A (a_rows >= M).  Else it is row
+ * index[r] / per of A and SA, which have a_rows rows: with moe_sort's src and per = top_k
+ * tokens are read where they lie.  (A row number past the end is taken as the last row of A, a
+ * negative one as row 0; offsets that do not ascend give unspecified results, but no
+ * access outside the arrays.)
+ */
+int i8_gemm_grouped(int groups, const int* offsets, int M, int N, int K, float alpha,
+                    const int8_t* A, int lda, const float* SA, int a_rows,
+                    const int* index, int per,
+                    const int8_t* B, int ldb, const float* SB,
+                    const float* bias, int act, int gated, int type, void* C, int ldc,
+                    hipStream_t stream);
+
+/* Bytes of device memory a moe_sort call of this shape needs as `workspace`. */
+int moe_sort_workspace(int tokens, int top_k, int experts, size_t* bytes);
+
+/*
+ * Tokens in the order of their experts: a stable sort of ids (tokens x top_k dense, the expert
+ * of every token's slots; numbers outside 0 .. experts - 1 are no expert's, as those of padding).
+ *   offsets[e] (experts + 1)       the first row of expert e; offsets[experts] rows in all,
+ *   src[row] (tokens x top_k)      the entry token * top_k + slot of every row, -1 behind the last,
+ *   pos[token][slot] (as ids)      the row of every entry, -1 for those of no expert.
+ * An expert's rows are in the order of their entries.  experts 1 .. 1024, top_k 1 .. 32,
+ * tokens x top_k at most 2^30; a token may name an expert twice.  `workspace` (256-byte
+ * aligned, at least moe_sort_workspace bytes) belongs to the call until its work on `stream`
+ * is done; its contents need no preparation.
+ */
+int moe_sort(int tokens, int top_k, int experts, const int* ids, int* offsets, int* src, int* pos,
+             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Tokens into sorted rows: Y[pos[t][s]] = X[t], times w[t][s] where w (FP32, tokens x top_k dense) is
+ * not NULL.  X tokens x cols (ldx), Y y_rows x cols (ldy), both of `type` F32, F16 or BF16;
+ * products fp32, rounded once.  Entries of pos outside 0 .. y_rows - 1 are
+ * skipped; rows of Y that none names are left as they were, and no two may name the same.
+ * Gradients: to X that is moe_combine of Y's gradient with the same pos and w, to w
+ * moe_combine_grad's dw with X for its dY and Y's gradient for its X.
+ */
+int moe_dispatch(int tokens, int top_k, int cols, int type, const void* X, int ldx,
+                 const int* pos, const float* w, void* Y, int ldy, int y_rows, hipStream_t stream);
+
+/*
+ * Sorted rows back to their tokens: Y[t] = sum_s w[t][s] X[pos[t][s]] (w NULL: ones), fp32 sums in the
+ * order of the slots, rounded once.  X x_rows x cols (ldx), Y tokens x cols (ldy).  Entries of
+ * pos outside 0 .. x_rows - 1 are skipped (whatever their w); a token without any is zero.
+ */
+int moe_combine(int tokens, int top_k, int cols, int type, const void* X, int ldx, int x_rows,
+                const int* pos, const float* w, void* Y, int ldy, hipStream_t stream);
+
+/*
+ * moe_combine's gradients:
+ *   dX[pos[t][s]] = w[t][s] dY[t],   dw[t][s] = sum_c dY[t][c] X[pos[t][s]][c],
+ * dw FP32 (tokens x top_k dense), 0 for entries outside 0 .. x_rows - 1; dX x_rows x cols (lddx), of
+ * which rows that no entry names are left as they were, and no two may name the same.  Either dX
+ * or dw may be NULL: then it is not wanted (without dw X is not read).  dX must not
+ * overlap X or dY.
+ */
+int moe_combine_grad(int tokens, int top_k, int cols, int type, const void* dY, int lddy,
+                     const void* X, int ldx, int x_rows, const int* pos, const float* w,
+                     void* dX, int lddx, float* dw, hipStream_t stream);
 
 /* Static text for a status code; for GEMM_STATUS_HIP_ERROR it also names the
  * last HIP error seen by the library on this host thread. */

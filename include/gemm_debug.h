@@ -50,6 +50,16 @@ extern "C" {
 int gemm_debug_force_tile(int op, int tile);
 
 /*
+ * Force the tile of later calls of i8_gemm_bias_act and i8_gemm_grouped: -1 = by
+ * shape (the default); 0 = 256 x 256, 1 = 128 x 128 and 2 = 64 x 64 rows of A and B, copied straight
+ * into LDS (where rows are off 16-byte boundaries, 3); 3 = 128 x 128 through registers; and
+ * tiles whose eight waves split K between them: 4 = 64 x 32, 5 = 64 x 16, 6 = 32 x 32, 7 =
+ * 32 x 16, 8 = 16 x 32, 9 = 16 x 16.  Returns GEMM_STATUS_INVALID_VALUE for another number.
+ * Pure host state, not synchronised with calls in flight on other threads.
+ */
+int gemm_debug_force_i8_tile(int tile);
+
+/*
  * Force how many rows of a weight a workgroup of moe_ffn's two products takes in
  * later calls: 0 = by shape (the default), else 16, 32 or 64, reduced to the
  * widest that the call's kernels have (the first product of a gated layer has 32,

@@ -16,8 +16,10 @@ import os
 
 __all__ = ["GemmError", "gemm_create", "gemm_destroy", "sgemm", "sgemm_noalloc", "hgemm_bias_act",
            "bgemm_bias_act", "fp8_quantize", "fp8_gemm_bias_act", "MoeShape", "moe_ffn_workspace",
-           "moe_ffn",
+           "moe_ffn", "i8_quantize", "i8_gemm_bias_act", "i8_gemm_grouped", "moe_sort_workspace",
+           "moe_sort", "moe_dispatch", "moe_combine", "moe_combine_grad",
            "gemm_status_string", "gemm_debug_force_tile", "gemm_debug_force_moe_rows",
+           "gemm_debug_force_i8_tile",
            "gemm_debug_force_splits",
            "gemm_debug_pick_config", "gemm_debug_use_tuned_table", "gemm_debug_force_swizzle",
            "gemm_debug_tile_map", "library_path",
@@ -36,7 +38,7 @@ STATUS_INTERNAL = 5
 
 ACT_NONE = 0
 ACT_GELU_TANH = 1
-ACT_SILU = 2   # fp8_gemm_bias_act and moe_ffn only
+ACT_SILU = 2   # the 8-bit products and moe_ffn only
 
 TYPE_F32 = 0
 TYPE_F16 = 1
@@ -46,8 +48,11 @@ TYPE_E4M3 = 3
 # Every symbol declared in include/gemm.h and include/gemm_debug.h.
 EXPORTED_SYMBOLS = ("gemm_create", "gemm_destroy", "sgemm", "sgemm_noalloc", "hgemm_bias_act",
                     "bgemm_bias_act", "fp8_quantize", "fp8_gemm_bias_act", "moe_ffn_workspace",
-                    "moe_ffn",
+                    "moe_ffn", "i8_quantize", "i8_gemm_bias_act", "i8_gemm_grouped",
+                    "moe_sort_workspace", "moe_sort", "moe_dispatch", "moe_combine",
+                    "moe_combine_grad",
                     "gemm_status_string", "gemm_debug_force_tile", "gemm_debug_force_moe_rows",
+                    "gemm_debug_force_i8_tile",
                     "gemm_debug_force_splits",
                     "gemm_debug_pick_config", "gemm_debug_use_tuned_table",
                     "gemm_debug_force_swizzle", "gemm_debug_tile_map")
@@ -102,6 +107,24 @@ def load_library():
     lib.moe_ffn_workspace.restype = I
     lib.moe_ffn.argtypes = [SP, P, I, P, I, P, I, P, P, I, P, P, P, P, I, P, S, P]
     lib.moe_ffn.restype = I
+    lib.i8_quantize.argtypes = [I, I, I, P, I, P, I, P, P]
+    lib.i8_quantize.restype = I
+    lib.i8_gemm_bias_act.argtypes = [I, I, I, F, P, I, P, P, I, P, P, I, I, I, P, I, P]
+    lib.i8_gemm_bias_act.restype = I
+    lib.i8_gemm_grouped.argtypes = [I, P, I, I, I, F, P, I, P, I, P, I, P, I, P, P, I, I, I, P, I, P]
+    lib.i8_gemm_grouped.restype = I
+    lib.moe_sort_workspace.argtypes = [I, I, I, ctypes.POINTER(S)]
+    lib.moe_sort_workspace.restype = I
+    lib.moe_sort.argtypes = [I, I, I, P, P, P, P, P, S, P]
+    lib.moe_sort.restype = I
+    lib.moe_dispatch.argtypes = [I, I, I, I, P, I, P, P, P, I, I, P]
+    lib.moe_dispatch.restype = I
+    lib.moe_combine.argtypes = [I, I, I, I, P, I, I, P, P, P, I, P]
+    lib.moe_combine.restype = I
+    lib.moe_combine_grad.argtypes = [I, I, I, I, P, I, P, I, I, P, P, P, I, P, P]
+    lib.moe_combine_grad.restype = I
+    lib.gemm_debug_force_i8_tile.argtypes = [I]
+    lib.gemm_debug_force_i8_tile.restype = I
     lib.gemm_status_string.argtypes = [I]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_debug_force_tile.argtypes = [I, I]
@@ -247,6 +270,78 @@ def moe_ffn(shape, X, ldx, R, ldr, W1, ld1, S1, W2, ld2, S2, ids, w, Y, ldy, wor
     return _check(st, "moe_ffn", raise_on_error)
 
 
+def i8_quantize(rows, cols, type, X, ldx, Q, ldq, S, stream=None, *, raise_on_error=True):
+    """Rows of X as int8 values and a scale for each row; see include/gemm.h."""
+    st = load_library().i8_quantize(int(rows), int(cols), int(type), _ptr(X), int(ldx), _ptr(Q),
+                                    int(ldq), _ptr(S), _stream(stream))
+    return _check(st, "i8_quantize", raise_on_error)
+
+
+def i8_gemm_bias_act(M, N, K, alpha, A, lda, SA, B, ldb, SB, bias, act, gated, type, C, ldc,
+                     stream=None, *, raise_on_error=True):
+    """C = act(alpha SA SB A x B^T + bias), int8 A and B with a scale for every row; gated: times the
+    product's second N columns; see include/gemm.h."""
+    st = load_library().i8_gemm_bias_act(int(M), int(N), int(K), float(alpha), _ptr(A), int(lda),
+                                         _ptr(SA), _ptr(B), int(ldb), _ptr(SB), _ptr(bias), int(act),
+                                         int(gated), int(type), _ptr(C), int(ldc), _stream(stream))
+    return _check(st, "i8_gemm_bias_act", raise_on_error)
+
+
+def i8_gemm_grouped(groups, offsets, M, N, K, alpha, A, lda, SA, a_rows, index, per, B, ldb, SB, bias,
+                    act, gated, type, C, ldc, stream=None, *, raise_on_error=True):
+    """i8_gemm_bias_act of rows in groups, each with a matrix of its own; see include/gemm.h."""
+    st = load_library().i8_gemm_grouped(int(groups), _ptr(offsets), int(M), int(N), int(K),
+                                        float(alpha), _ptr(A), int(lda), _ptr(SA), int(a_rows),
+                                        _ptr(index), int(per), _ptr(B), int(ldb), _ptr(SB),
+                                        _ptr(bias), int(act), int(gated), int(type), _ptr(C),
+                                        int(ldc), _stream(stream))
+    return _check(st, "i8_gemm_grouped", raise_on_error)
+
+
+def moe_sort_workspace(tokens, top_k, experts) -> int:
+    """Bytes of device memory a moe_sort call of this shape needs as its workspace."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_sort_workspace(int(tokens), int(top_k), int(experts), ctypes.byref(n)),
+           "moe_sort_workspace", True)
+    return n.value
+
+
+def moe_sort(tokens, top_k, experts, ids, offsets, src, pos, workspace, workspace_bytes, stream=None,
+             *, raise_on_error=True):
+    """Entries (token, slot) in the order of their experts; see include/gemm.h."""
+    st = load_library().moe_sort(int(tokens), int(top_k), int(experts), _ptr(ids), _ptr(offsets),
+                                 _ptr(src), _ptr(pos), _ptr(workspace), int(workspace_bytes),
+                                 _stream(stream))
+    return _check(st, "moe_sort", raise_on_error)
+
+
+def moe_dispatch(tokens, top_k, cols, type, X, ldx, pos, w, Y, ldy, y_rows, stream=None, *,
+                 raise_on_error=True):
+    """Y[pos[t][s]] = X[t], times w[t][s] if given; see include/gemm.h."""
+    st = load_library().moe_dispatch(int(tokens), int(top_k), int(cols), int(type), _ptr(X), int(ldx),
+                                     _ptr(pos), _ptr(w), _ptr(Y), int(ldy), int(y_rows),
+                                     _stream(stream))
+    return _check(st, "moe_dispatch", raise_on_error)
+
+
+def moe_combine(tokens, top_k, cols, type, X, ldx, x_rows, pos, w, Y, ldy, stream=None, *,
+                raise_on_error=True):
+    """Y[t] = sum_s w[t][s] X[pos[t][s]]; see include/gemm.h."""
+    st = load_library().moe_combine(int(tokens), int(top_k), int(cols), int(type), _ptr(X), int(ldx),
+                                    int(x_rows), _ptr(pos), _ptr(w), _ptr(Y), int(ldy),
+                                    _stream(stream))
+    return _check(st, "moe_combine", raise_on_error)
+
+
+def moe_combine_grad(tokens, top_k, cols, type, dY, lddy, X, ldx, x_rows, pos, w, dX, lddx, dw,
+                     stream=None, *, raise_on_error=True):
+    """moe_combine's gradients to its rows and its weights; see include/gemm.h."""
+    st = load_library().moe_combine_grad(int(tokens), int(top_k), int(cols), int(type), _ptr(dY),
+                                         int(lddy), _ptr(X), int(ldx), int(x_rows), _ptr(pos),
+                                         _ptr(w), _ptr(dX), int(lddx), _ptr(dw), _stream(stream))
+    return _check(st, "moe_combine_grad", raise_on_error)
+
+
 def gemm_status_string(status: int) -> str:
     try:
         return load_library().gemm_status_string(int(status)).decode()
@@ -260,6 +355,10 @@ def gemm_debug_force_tile(op: int, tile: int) -> int:
 
 def gemm_debug_force_moe_rows(rows: int) -> int:
     return load_library().gemm_debug_force_moe_rows(int(rows))
+
+
+def gemm_debug_force_i8_tile(tile: int) -> int:
+    return load_library().gemm_debug_force_i8_tile(int(tile))
 
 
 def gemm_debug_force_splits(op: int, splits: int) -> int:

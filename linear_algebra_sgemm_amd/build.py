@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["gemm_capi.cpp", "gemm_config.cpp", "sgemm_kernels.hip", "hgemm_kernels.hip",
            "pack_kernels.hip", "lm_capi.cpp", "quantize_kernels.hip", "fp8_kernels.hip",
-           "fp8_tile_kernels.hip", "moe_kernels.hip"]
+           "fp8_tile_kernels.hip", "moe_kernels.hip", "i8_quantize_kernels.hip", "i8_kernels.hip",
+           "i8_tile_kernels.hip", "exchange_kernels.hip"]
 ARCH = "gfx950"
 
 DEVICE_FLAGS = [

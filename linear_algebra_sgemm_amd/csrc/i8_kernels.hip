@@ -1,0 +1,315 @@
+// The int8 product with a scale for every token and channel:
+//     u[m][n] = alpha sa[m] sb[n] sum_k A[m][k] B[n][k] + bias[n],   C = act(u),
+// or with a gate (B has 2 N rows)  C[m][n] = act(u[m][n]) u[m][N + n];  A (M x K)
+// and B (N x K) in int8, both contiguous along K.  Grouped: the rows of A are those of
+// one group after the other, and B, sb and bias are their group's.
+//
+// The sums are int32 and exact (K <= 131071: 2^17 products of -128 and -128 would
+// pass 2^31 - 1), so neither the order nor the split of K changes a result.
+// Each is rounded to fp32 once, then scaled.
+//
+// Operand k order: an MFMA pairs the same lane and byte of both operands, so
+// any assignment of k to lanes serves if both use it.
+#include "i8_common.h"
+
+namespace lasg {
+
+namespace {
+
+// One 16-row fragment of 128 k: lane l holds row l % 16, the 16-byte chunks
+// l / 16 and l / 16 + 4 of its eight.
+struct Frag8 {
+  u32x4 c[2];
+};
+
+__device__ __forceinline__ void load_frag(Frag8& f, const int8_t* row, int lane, int k0) {
+  const int k = k0 + 16 * (lane / 16);
+  f.c[0] = load16(row + k);
+  f.c[1] = load16(row + k + 64);
+}
+// The same at the end of a row of K bytes.
+__device__ __forceinline__ void load_frag_tail(Frag8& f, const int8_t* row, int lane, int k0, int K) {
+  const int k = k0 + 16 * (lane / 16);
+  f.c[0] = load16_row(row, k, K);
+  f.c[1] = load16_row(row, k + 64, K);
+}
+
+__device__ __forceinline__ i32x4 add_product(const Frag8& x, const Frag8& y, i32x4 acc) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, x.c[h]),
+                                                __builtin_bit_cast(i32x4, y.c[h]), acc, 0, 0, 0);
+  return acc;
+}
+
+// Four consecutive values of one row of C (columns col ..; `left` of them exist).
+__device__ __forceinline__ void store_c(const I8Call& p, int64_t row, int64_t col, f32x4 v) {
+  const int64_t left = p.N - col;
+  if (p.type == GEMM_TYPE_F32) {
+    float* d = static_cast<float*>(p.C) + row * p.ldc + col;
+    if (left >= 4) {
+      *reinterpret_cast<f32x4_any*>(d) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) d[e] = v[e];
+    }
+    return;
+  }
+  uint16_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    h[e] = p.type == GEMM_TYPE_F16 ? LmF16::bits(v[e]) : LmBF16::bits(v[e]);
+  uint16_t* d = static_cast<uint16_t*>(p.C) + row * p.ldc + col;
+  if (left >= 4) {
+    *reinterpret_cast<u32x2_any*>(d) = __builtin_bit_cast(u32x2, h);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) d[e] = h[e];
+  }
+}
+
+}  // namespace
+
+// A tile of 16 MF rows of A by 16 NF rows of B per workgroup, its eight waves taking
+// an eighth of the blocks of 128 k each, straight from memory into MFMA operands, the
+// eight sums added in LDS at the end.  Any shape, stride and alignment.  Few rows:
+// the bytes of B bound it, every one of which is read once; what matters is
+// how many are on their way.  A wave loads GROUP blocks before it multiplies the first,
+// and with many fragments the next block of B while it multiplies this one.
+// With a gate the 16 rows of a fragment of B are eight of each half, so that
+// a result's two sums lie 32 lanes apart in one fragment.
+template <int MF, int NF, bool GROUPED>
+__global__ void __launch_bounds__(512) i8_ksplit_kernel(I8Call p) {
+  constexpr int GROUP = MF + NF <= 3 ? 4 : MF * NF <= 4 ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) i32x4 part[4][MF * NF][kWave];
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = lane % 16, g = lane / 16;
+  const int64_t b_rows = i8_b_rows(p);
+  const unsigned tiles_n = (unsigned)((b_rows + 16 * NF - 1) / (16 * NF));
+  int64_t total;
+  GroupTiles<16 * MF> tiles(p);
+  if constexpr (GROUPED)
+    total = (int64_t)tiles.total * tiles_n;
+  else
+    total = (((int64_t)p.M + 16 * MF - 1) / (16 * MF)) * tiles_n;
+  const int full = p.K / kBlockK;
+  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+    const unsigned tm = (unsigned)(t / tiles_n), tn = (unsigned)(t - (int64_t)tm * tiles_n);
+    int group = 0, m0 = (int)(tm * 16 * MF), m_end = p.M;
+    if constexpr (GROUPED) {
+      tiles.find(p, (int)tm, group, m0, m_end);
+      if (m0 >= m_end) continue;
+    }
+    const int8_t* b_mat = p.B + group * b_rows * p.ldb;
+    const float* sb_v = p.SB + group * b_rows;
+    const float* bias_v = p.bias == nullptr ? nullptr : p.bias + group * b_rows;
+    // The row of B behind row x of fragment j (past the end: the last; not stored).
+    const auto b_row = [&](int j, int x) -> int64_t {
+      const int64_t f = (int64_t)tn * NF + j;
+      if (!p.gated) {
+        const int64_t row = 16 * f + x;
+        return row < p.N ? row : p.N - 1;
+      }
+      const int64_t row = 8 * f + x % 8;
+      return (row < p.N ? row : p.N - 1) + (x >= 8 ? p.N : 0);
+    };
+    const int8_t* ap[MF];
+    const int8_t* bp[NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      const int row = m0 + 16 * i + r < m_end ? m0 + 16 * i + r : m_end - 1;
+      ap[i] = p.A + i8_a_row(p, row) * p.lda;
+    }
+#pragma unroll
+    for (int j = 0; j < NF; ++j) bp[j] = b_mat + b_row(j, r) * p.ldb;
+    i32x4 sums[MF * NF];
+#pragma unroll
+    for (int f = 0; f < MF * NF; ++f) sums[f] = i32x4{0, 0, 0, 0};
+    // (B first: the lane then holds four columns of one row of C)
+    const auto multiply = [&](const Frag8 (&a)[MF], const Frag8 (&b)[NF])
+        __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) sums[i * NF + j] = add_product(b[j], a[i], sums[i * NF + j]);
+    };
+    const auto load_a = [&](Frag8 (&a)[MF], int k0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < MF; ++i) load_frag(a[i], ap[i], lane, k0);
+    };
+    const auto load_b = [&](Frag8 (&b)[NF], int k0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < NF; ++j) load_frag(b[j], bp[j], lane, k0);
+    };
+    const int first = (int)((int64_t)full * wave / 8), end = (int)((int64_t)full * (wave + 1) / 8);
+    if constexpr (GROUP > 1) {
+      for (int kb = first; kb < end; kb += GROUP) {
+        Frag8 a[GROUP][MF], b[GROUP][NF];
+#pragma unroll
+        for (int u = 0; u < GROUP; ++u) {
+          const int at = kb + u < end ? kb + u : end - 1;   // (an extra read, not used)
+          load_b(b[u], at * kBlockK);
+          load_a(a[u], at * kBlockK);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < GROUP; ++u)
+          if (kb + u < end) multiply(a[u], b[u]);
+      }
+    } else if (first < end) {
+      Frag8 b[2][NF];
+      load_b(b[0], first * kBlockK);
+      // Two blocks a turn, so that the buffers of B keep their registers.
+      for (int kb = first; kb < end; kb += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (kb + u >= end) break;
+          Frag8 a[MF];
+          load_a(a, (kb + u) * kBlockK);
+          load_b(b[1 - u], (kb + u + 1 < end ? kb + u + 1 : kb + u) * kBlockK);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(a, b[u]);
+        }
+      }
+    }
+    if (full * kBlockK < p.K && wave == 7) {   // the last, shorter block
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        Frag8 b;
+        load_frag_tail(b, bp[j], lane, full * kBlockK, p.K);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          Frag8 a;
+          load_frag_tail(a, ap[i], lane, full * kBlockK, p.K);
+          sums[i * NF + j] = add_product(b, a, sums[i * NF + j]);
+        }
+      }
+    }
+    // Waves 4 to 7 put their sums down, waves 0 to 3 add theirs (half the space).
+    if (wave >= 4) {
+#pragma unroll
+      for (int f = 0; f < MF * NF; ++f) part[wave - 4][f][lane] = sums[f];
+    }
+    __syncthreads();
+    if (wave < 4) {
+#pragma unroll
+      for (int f = 0; f < MF * NF; ++f) part[wave][f][lane] += sums[f];
+    }
+    __syncthreads();
+    for (int f = wave; f < MF * NF; f += 8) {
+      const int i = f / NF, j = f % NF;
+      const int row = m0 + 16 * i + r;
+      const bool live = row < m_end && (!p.gated || g < 2);
+      if (!live) continue;
+      const SplitScale sa(p.K == 0 ? 0.0f : p.SA[i8_a_row(p, row)]);
+      // This lane's four columns of B (with a gate their counterparts are 32 lanes on).
+      const auto value = [&](int l, f32x4& u) __attribute__((always_inline)) {
+        const i32x4 v = (part[0][f][l] + part[1][f][l]) + (part[2][f][l] + part[3][f][l]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t n = b_row(j, 4 * (l / 16) + e);
+          const SplitScale sb(p.K == 0 ? 0.0f : sb_v[n]);
+          u[e] = i8_scaled(v[e], sa.m, sa.e, sb.m, sb.e, p.alpha, bias_v != nullptr ? bias_v[n] : 0.0f);
+        }
+      };
+      f32x4 v;
+      value(lane, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = apply_act(v[e], p.act);
+      int64_t col = ((int64_t)tn * NF + j) * 16 + 4 * g;
+      if (p.gated) {
+        f32x4 u;
+        value(lane + 32, u);
+        v *= u;
+        col = ((int64_t)tn * NF + j) * 8 + 4 * g;
+      }
+      if (col < p.N) store_c(p, row, col, v);
+    }
+    __syncthreads();   // the next tile reuses the LDS array
+  }
+}
+
+namespace {
+
+template <int MF, int NF>
+hipError_t launch_ksplit(const I8Call& c, hipStream_t s) {
+  const int64_t tn = (i8_b_rows(c) + 16 * NF - 1) / (16 * NF);
+  const int64_t total = i8_tiles_m(c, 16 * MF) * tn;
+  const unsigned grid = (unsigned)(total < (1 << 22) ? total : 1 << 22);
+  if (c.groups > 0)
+    i8_ksplit_kernel<MF, NF, true><<<grid, 512, 0, s>>>(c);
+  else
+    i8_ksplit_kernel<MF, NF, false><<<grid, 512, 0, s>>>(c);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// The rule takes the tile of the least estimated time.
+int i8_tile(const I8Call& c, int cus, int force) {
+  const int64_t b_rows = i8_b_rows(c);
+  // Rows a group: as if they were evenly spread.
+  const int64_t groups = c.groups > 0 ? (c.groups < c.M ? c.groups : c.M) : 1;
+  const int64_t rows = (c.M + groups - 1) / groups;
+  const auto tiles = [&](int m, int n) {
+    return groups * ((rows + m - 1) / m) * ((b_rows + n - 1) / n);
+  };
+  // 32-bit row, column and tile numbers in the tiled kernels.
+  const bool tiled = c.M <= (1 << 30) && b_rows <= (1 << 30) &&
+                     i8_tiles_m(c, 64) * ((b_rows + 63) / 64) < (1 << 23);
+  const bool direct = i8_direct(c);
+  static const int kSplit[6][2] = {{64, 32}, {64, 16}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
+  int tile = force;
+  if (tile < 0) {
+    double best = 1e30;
+    const auto offer = [&](int t, double cost) {
+      if (cost < best) {
+        best = cost;
+        tile = t;
+      }
+    };
+    if (tiled) {
+      // (start and end count as two blocks)
+      const double blocks = (double)(((int64_t)c.K + kBlockK - 1) / kBlockK) + 2;
+      const auto ring = [&](int m, int n, double one, double two) {
+        const double per_cu = (double)tiles(m, n) / cus;
+        return blocks * (per_cu <= 1 ? one : per_cu <= 2 ? two : two * per_cu / 2);
+      };
+      const double t128 = ring(128, 128, 700, 900);
+      if (direct) {
+        const double per_cu = (double)((tiles(256, 256) + cus - 1) / cus);
+        offer(0, blocks * 1500 * per_cu);
+        offer(1, t128);
+        offer(2, ring(64, 64, 500, 550));
+      } else {
+        offer(3, 2 * t128);
+      }
+    }
+    for (int i = 0; i < 6; ++i) {
+      const int m = kSplit[i][0], n = kSplit[i][1];
+      const double rounds = (double)((tiles(m, n) + cus - 1) / cus);
+      offer(4 + i, rounds * (m + n) * ((double)c.K + 512) / 23);
+    }
+  }
+  if (tile < 4 && !tiled) tile = 4;
+  if (tile < 3 && !direct) tile = 3;
+  return tile;
+}
+
+hipError_t launch_i8_gemm(const I8Call& c, int cus, int force, hipStream_t s) {
+  const int tile = i8_tile(c, cus, force);
+  switch (tile) {
+    case 4: return launch_ksplit<4, 2>(c, s);
+    case 5: return launch_ksplit<4, 1>(c, s);
+    case 6: return launch_ksplit<2, 2>(c, s);
+    case 7: return launch_ksplit<2, 1>(c, s);
+    case 8: return launch_ksplit<1, 2>(c, s);
+    case 9: return launch_ksplit<1, 1>(c, s);
+    default: return launch_i8_tile(c, tile, s);
+  }
+}
+
+}  // namespace lasg

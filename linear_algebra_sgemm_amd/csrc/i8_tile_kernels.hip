@@ -1,0 +1,423 @@
+// The int8 product in output tiles staged through LDS (formula: i8_kernels.hip),
+// for outputs large enough that the matrix units bound it.
+//
+// A K tile is 128 columns: rows of 128 bytes, copied from memory straight into LDS
+// (16 bytes a lane, whole 128-byte lines) STAGES tiles ahead.  Row r's eight 16-byte
+// chunks lie permuted by (r / 2) % 8, so that the fragment reads of 16 neighbouring rows
+// fall into 16 different bank groups.
+//
+// A wave multiplies 32x32 blocks, 32 columns of K a step, four steps a K tile: a step's
+// fragments are read while the step before is multiplied, those of the next K
+// tile's first step too, so a K tile has one meeting of the waves, before its last
+// step: there all have read tile t whole (its stage takes tile t + STAGES from then on) and
+// tile t + 1 has landed.  B is the first operand, so a lane holds the columns 8 q +
+// 4 (lane / 32) + 0..3 of one row of C.  With a gate, every 32 rows of B in the tile are
+// 16 of the first half and 16 of the second, so that both sums of a result
+// are one lane's.
+#include <type_traits>
+
+#include "dma_common.h"
+#include "i8_common.h"
+
+namespace lasg {
+
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, bool DIRECT_, bool GROUPED_>
+struct I8Tile {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+  static constexpr int STAGES = STAGES_;
+  static constexpr bool DIRECT = DIRECT_, GROUPED = GROUPED_;
+  static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = WAVES * kWave;
+  static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
+  static constexpr int FM = WTM / 32, FN = WTN / 32, BLOCKS = FM * FN;
+  static constexpr int A_BYTES = BM * kBlockK, STAGE_BYTES = (BM + BN) * kBlockK;
+  static constexpr int A_LOADS = BM / 8 / WAVES, B_LOADS = BN / 8 / WAVES;   // per wave, 1 KiB each
+  static constexpr int LOADS = A_LOADS + B_LOADS;
+  // Epilogue: 32 rows of each wave's results, then the scales (split) and bias.
+  static constexpr int REGION = 32 * WTN * 4;
+  static constexpr int SCALES_AT = WAVES * REGION;
+  static constexpr int EPILOGUE_BYTES = SCALES_AT + 4 * (3 * BN + 2 * BM);
+  static constexpr int LDS_BYTES =
+      STAGES * STAGE_BYTES > EPILOGUE_BYTES ? STAGES * STAGE_BYTES : EPILOGUE_BYTES;
+  static_assert(DIRECT || STAGES == 2, "through registers one tile ahead");
+  static_assert(STAGES >= 2 && (STAGES - 1) * LOADS <= 63, "copies on their way must fit vmcnt");
+  static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "copies split evenly over waves");
+  static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tile");
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+};
+
+struct I8TileArgs {
+  I8Call c;
+  int tiles_m, tiles_n, group_m;
+};
+
+namespace {
+
+template <class T>
+struct I8Frags {
+  i32x4 a[T::FM], b[T::FN];
+};
+
+// The results of a wave, 32 rows at a time: scales, bias, activation and gate in
+// registers, rounded to C's type, through the wave's own piece of LDS (chunks permuted as
+// above) so that whole rows are stored, 16 bytes a lane.
+template <class T, int ACT, bool WIDE, bool GATED>
+__device__ __forceinline__ void i8_write_back(const I8Call& c, const i32x16 (&sum)[T::FM][T::FN],
+                                              uint8_t* lds, int wave, int m0, int m_end, int n0,
+                                              int lane) {
+  constexpr int WIDTH = GATED ? T::WTN / 2 : T::WTN;   // columns of C
+  constexpr int SIZE = WIDE ? 4 : 2, ROW = WIDTH * SIZE, CHUNKS = ROW / 16;
+  constexpr int LINE = ROW >= 256 ? 1 : 256 / ROW;     // rows in a line of the LDS banks
+  static_assert(1024 % ROW == 0, "whole rows per store");
+  const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+  const int l32 = lane % 32, half = lane / 32;
+  uint8_t* region = lds + wave * T::REGION;
+  const float* mb = reinterpret_cast<const float*>(lds + T::SCALES_AT) + wn * T::WTN + 4 * half;
+  const int* eb = reinterpret_cast<const int*>(mb + T::BN);
+  const float* bias = mb + 2 * T::BN;
+  const float* ma = reinterpret_cast<const float*>(lds + T::SCALES_AT) + 3 * T::BN + wm * T::WTM + l32;
+  const int* ea = reinterpret_cast<const int*>(ma + T::BM);
+  const bool f16 = c.type == GEMM_TYPE_F16;
+  const int col0 = n0 + wn * WIDTH;
+  auto slot = [](int row, int chunk) {
+    return row * ROW + 16 * (chunk ^ (row / LINE & (CHUNKS - 1)));
+  };
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) {
+    const float ma_i = ma[32 * i];
+    const int ea_i = ea[32 * i];
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int q = 0; q < (GATED ? 2 : 4); ++q) {
+        // (`x`: columns x .. x + 3 of the fragment, whose sums are registers x / 2 ..)
+        const auto scaled = [&](int x) __attribute__((always_inline)) {
+          const f32x4 m4 = *reinterpret_cast<const f32x4*>(mb + 32 * j + x);
+          const i32x4 e4 = *reinterpret_cast<const i32x4*>(eb + 32 * j + x);
+          const f32x4 b4 = *reinterpret_cast<const f32x4*>(bias + 32 * j + x);
+          f32x4 u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            u[e] = i8_scaled(sum[i][j][x / 2 + e], ma_i, ea_i, m4[e], e4[e], c.alpha, b4[e]);
+          return u;
+        };
+        f32x4 v = scaled(8 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = apply_act(v[e], ACT);
+        if constexpr (GATED) {
+          const f32x4 u = scaled(8 * q + 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] *= u[e];
+        }
+        const int at = (GATED ? 16 : 32) * j + 8 * q + 4 * half;   // column in the wave's tile
+        if constexpr (WIDE) {
+          *reinterpret_cast<f32x4*>(region + slot(l32, at / 4)) = v;
+        } else {
+          uint16_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = f16 ? LmF16::bits(v[e]) : LmBF16::bits(v[e]);
+          *reinterpret_cast<u32x2*>(region + slot(l32, at / 8) + 8 * half) =
+              __builtin_bit_cast(u32x2, h);
+        }
+      }
+    asm volatile("" ::: "memory");   // (one wave's LDS accesses keep their order)
+    constexpr int ROWS = 1024 / ROW < 32 ? 1024 / ROW : 32;   // of a store
+#pragma unroll
+    for (int it = 0; it < 32 / ROWS; ++it) {
+      const int r = it * ROWS + lane / CHUNKS, chunk = lane % CHUNKS;
+      if (1024 / ROW > 32 && r >= 32) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(region + slot(r, chunk));
+      const int row = m0 + wm * T::WTM + 32 * i + r, col = col0 + chunk * (16 / SIZE);
+      if (row >= m_end || col >= c.N) continue;
+      uint8_t* d = static_cast<uint8_t*>(c.C) + ((int64_t)row * c.ldc + col) * SIZE;
+      if (col + 16 / SIZE <= c.N) {
+        *reinterpret_cast<u32x4_any*>(d) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16 / SIZE; ++e)
+          if (col + e < c.N) {
+            if constexpr (WIDE)
+              reinterpret_cast<uint32_t*>(d)[e] = v[e % 4];
+            else
+              reinterpret_cast<uint16_t*>(d)[e] = (uint16_t)(v[e / 2 % 4] >> (16 * (e & 1)));
+          }
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+}
+
+template <class T, int ACT>
+__device__ __forceinline__ void i8_write_as(const I8Call& c, const i32x16 (&sum)[T::FM][T::FN],
+                                            uint8_t* lds, int wave, int m0, int m_end, int n0,
+                                            int lane) {
+  if (c.type == GEMM_TYPE_F32)
+    c.gated ? i8_write_back<T, ACT, true, true>(c, sum, lds, wave, m0, m_end, n0, lane)
+            : i8_write_back<T, ACT, true, false>(c, sum, lds, wave, m0, m_end, n0, lane);
+  else
+    c.gated ? i8_write_back<T, ACT, false, true>(c, sum, lds, wave, m0, m_end, n0, lane)
+            : i8_write_back<T, ACT, false, false>(c, sum, lds, wave, m0, m_end, n0, lane);
+}
+
+}  // namespace
+
+template <class T>
+__global__ void __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(2)))
+i8_tile_kernel(I8TileArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS_BYTES];
+  const I8Call& c = p.c;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+  const int l32 = lane % 32, half = lane / 32;
+  const uint32_t lds_base = lds_offset(lds);
+  const int b_rows = (int)i8_b_rows(c);
+  int tile_m, tile_n, m0, m_end = c.M, group = 0;
+  if constexpr (T::GROUPED) {
+    const GroupTiles<T::BM> tiles(c);
+    if ((int64_t)blockIdx.x >= (int64_t)tiles.total * p.tiles_n) return;
+    tile_of_workgroup(blockIdx.x, tiles.total, p.tiles_n, p.group_m, tile_m, tile_n);
+    tiles.find(c, tile_m, group, m0, m_end);
+    if (m0 >= m_end) return;
+  } else {
+    tile_of_workgroup(blockIdx.x, p.tiles_m, p.tiles_n, p.group_m, tile_m, tile_n);
+    m0 = tile_m * T::BM;
+  }
+  // First column of C; the tile's first row of B (of each half, with a gate).
+  const int n0 = tile_n * (c.gated ? T::BN / 2 : T::BN);
+  const int64_t group_b = (int64_t)group * b_rows;
+  const int8_t* b_tile = c.B + (group_b + n0) * c.ldb;
+  // Rows of A from where the tile begins, or anywhere in A.
+  const int8_t* a_tile = c.index != nullptr ? c.A : c.A + (int64_t)m0 * c.lda;
+  const int kts = (c.K + kBlockK - 1) / kBlockK;
+
+  // The row of A (from a_tile) or B (from b_tile) that tile row `row` is; past the
+  // end the last.
+  auto a_row = [&](int row) __attribute__((always_inline)) {
+    const int r = m0 + row < m_end ? row : m_end - 1 - m0;
+    return c.index != nullptr ? i8_a_row(c, m0 + r) : (int64_t)r;
+  };
+  auto b_row = [&](int row) __attribute__((always_inline)) {
+    const int at = c.gated ? row / 32 * 16 + row % 16 : row;
+    const int r = n0 + at < c.N ? at : c.N - 1 - n0;
+    return c.gated && (row & 16) ? r + c.N : r;
+  };
+  // Row (of the tile) and chunk that lane `l` copies in load v of this wave.
+  auto slot = [&](int v, int l, int& row, int& chunk) __attribute__((always_inline)) {
+    row = 8 * (v < T::A_LOADS ? wave * T::A_LOADS + v : wave * T::B_LOADS + v - T::A_LOADS) + l / 8;
+    chunk = (l % 8) ^ ((row >> 1) & 7);
+  };
+  auto slot_at = [&](int v, int t) __attribute__((always_inline)) {
+    return t % T::STAGES * T::STAGE_BYTES +
+           (v < T::A_LOADS ? (wave * T::A_LOADS + v) * 1024
+                           : T::A_BYTES + (wave * T::B_LOADS + v - T::A_LOADS) * 1024);
+  };
+  // K tiles in the order they are taken.  A last, shorter one goes through registers, with zeros
+  // behind it; where whole ones are copied straight into LDS it is taken first, so that its
+  // latency falls together with the first copies'.
+  const bool tail_first = T::DIRECT && c.K % kBlockK != 0;
+  auto block_of = [&](int t) __attribute__((always_inline)) {
+    return !tail_first ? t : t == 0 ? kts - 1 : t - 1;
+  };
+  uint32_t off[T::DIRECT ? T::LOADS : 1];
+  if constexpr (T::DIRECT) {
+#pragma unroll
+    for (int v = 0; v < T::LOADS; ++v) {
+      int row, chunk;
+      slot(v, lane, row, chunk);
+      off[v] = (uint32_t)(v < T::A_LOADS ? a_row(row) * c.lda : (int64_t)b_row(row) * c.ldb) +
+               16 * chunk;
+    }
+  }
+  auto copy = [&](int t, int v) __attribute__((always_inline)) {
+    dma16_sbase_u((v < T::A_LOADS ? a_tile : b_tile) + block_of(t) * kBlockK, off[v],
+                  lds_base + slot_at(v, t));
+  };
+  // K tile t through registers, any alignment: loaded, and later stored.
+  u32x4 held[T::DIRECT ? 1 : T::LOADS];
+  auto load_one = [&](int t, int v) __attribute__((always_inline)) {
+    int row, chunk;
+    slot(v, lane, row, chunk);
+    const int8_t* at = v < T::A_LOADS ? a_tile + a_row(row) * c.lda
+                                      : b_tile + (int64_t)b_row(row) * c.ldb;
+    const int k = block_of(t) * kBlockK + 16 * chunk;
+    return block_of(t) * kBlockK + kBlockK <= c.K ? load16(at + k) : load16_row(at, k, c.K);
+  };
+  auto copy_by_hand = [&](int t) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int v = 0; v < T::LOADS; ++v)
+      *reinterpret_cast<u32x4*>(lds + slot_at(v, t) + 16 * lane) = load_one(t, v);
+  };
+
+  i32x16 sum[T::FM][T::FN];
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) sum[i][j] = i32x16{};
+
+  // This lane's chunk of a fragment row in step s is (2 s + half) permuted.
+  const uint32_t swizzled = 16 * (half ^ ((l32 >> 1) & 7));
+  const uint32_t a_frag = (wm * T::WTM + l32) * kBlockK;
+  const uint32_t b_frag = T::A_BYTES + (wn * T::WTN + l32) * kBlockK;
+  auto read = [&](I8Frags<T>& f, int t, int s) __attribute__((always_inline)) {
+    const uint8_t* st = lds + t % T::STAGES * T::STAGE_BYTES + (swizzled ^ (32 * s));
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+      f.a[i] = *reinterpret_cast<const i32x4*>(st + a_frag + i * 32 * kBlockK);
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+      f.b[j] = *reinterpret_cast<const i32x4*>(st + b_frag + j * 32 * kBlockK);
+  };
+  auto multiply = [&](const I8Frags<T>& f, int x) __attribute__((always_inline)) {
+    const int i = x / T::FN, j = x % T::FN;
+    sum[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[i], sum[i][j], 0, 0, 0);
+  };
+  I8Frags<T> f0, f1;
+
+  // K tile t, whose first step's fragments are in f0; COPY: with the copies of tile t +
+  // STAGES; MORE: tile t + 1 follows.
+  constexpr int PRE = T::BLOCKS >= 4 ? 2 : 1;   // MFMAs that run while the waves meet
+  auto k_tile = [&](int t, auto copy_next, auto more) __attribute__((always_inline)) {
+    constexpr bool COPY = decltype(copy_next)::value, MORE = decltype(more)::value;
+    read(f1, t, 1);
+    if constexpr (!T::DIRECT && MORE) {
+#pragma unroll
+      for (int v = 0; v < T::LOADS; ++v) held[v] = load_one(t + 1, v);
+    }
+#pragma unroll
+    for (int x = 0; x < T::BLOCKS; ++x) multiply(f0, x);
+    __builtin_amdgcn_sched_barrier(0);
+    read(f0, t, 2);
+#pragma unroll
+    for (int x = 0; x < T::BLOCKS; ++x) multiply(f1, x);
+    __builtin_amdgcn_sched_barrier(0);
+    read(f1, t, 3);
+#pragma unroll
+    for (int x = 0; x < T::BLOCKS; ++x) multiply(f0, x);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!T::DIRECT && MORE) {
+#pragma unroll
+      for (int v = 0; v < T::LOADS; ++v)
+        *reinterpret_cast<u32x4*>(lds + slot_at(v, t + 1) + 16 * lane) = held[v];
+    }
+#pragma unroll
+    for (int x = 0; x < PRE; ++x) multiply(f1, x);
+    if constexpr (MORE) {
+      // Tile t + 1 has landed (younger copies may be on their way) and tile t is read.
+      if constexpr (COPY)
+        wait_vmcnt<(T::STAGES - 2) * T::LOADS>();
+      else
+        wait_vmcnt<0>();
+      lds_barrier();
+      read(f0, t + 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // The copies between the last MFMAs (all at once would hold every wave at issue).
+    constexpr int REST = T::BLOCKS - PRE;
+#pragma unroll
+    for (int x = 0; x < REST || (x == 0 && REST == 0); ++x) {
+      if (x < REST) multiply(f1, PRE + x);
+      if constexpr (COPY) {
+        constexpr int OVER = REST > 0 ? REST : 1;
+#pragma unroll
+        for (int v = x * T::LOADS / OVER; v < (x + 1) * T::LOADS / OVER; ++v) copy(t + T::STAGES, v);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (kts > 0) {
+    if constexpr (T::DIRECT) {
+#pragma unroll
+      for (int first = 0; first < T::STAGES; ++first) {
+        if (first >= kts) break;
+        if (first == 0 && tail_first) {
+          copy_by_hand(0);
+        } else {
+#pragma unroll
+          for (int v = 0; v < T::LOADS; ++v) copy(first, v);
+        }
+      }
+      if (kts >= T::STAGES)
+        wait_vmcnt<(T::STAGES - 1) * T::LOADS>();
+      else
+        wait_vmcnt<0>();
+    } else {
+      copy_by_hand(0);
+    }
+    lds_barrier();
+    read(f0, 0, 0);
+    int t = 0;
+    if constexpr (T::DIRECT)
+      for (; t + T::STAGES < kts; ++t) k_tile(t, std::true_type(), std::true_type());
+    for (; t + 1 < kts; ++t) k_tile(t, std::false_type(), std::true_type());
+    k_tile(t, std::false_type(), std::false_type());
+  }
+
+  lds_barrier();   // every wave is done reading the stages
+  {
+    float* mb = reinterpret_cast<float*>(lds + T::SCALES_AT);
+    for (int x = threadIdx.x; x < T::BN; x += T::THREADS) {
+      const int64_t n = group_b + n0 + b_row(x);
+      const SplitScale s(c.K == 0 ? 0.0f : c.SB[n]);
+      mb[x] = s.m;
+      reinterpret_cast<int*>(mb)[T::BN + x] = s.e;
+      mb[2 * T::BN + x] = c.bias != nullptr ? c.bias[n] : 0.0f;
+    }
+    float* ma = mb + 3 * T::BN;
+    for (int x = threadIdx.x; x < T::BM; x += T::THREADS) {
+      const int64_t a = a_row(x) + (c.index != nullptr ? 0 : m0);
+      const SplitScale s(c.K == 0 ? 0.0f : c.SA[a]);
+      ma[x] = s.m;
+      reinterpret_cast<int*>(ma)[T::BM + x] = s.e;
+    }
+  }
+  lds_barrier();
+  if (c.act == GEMM_ACT_NONE)
+    i8_write_as<T, 0>(c, sum, lds, wave, m0, m_end, n0, lane);
+  else if (c.act == GEMM_ACT_GELU_TANH)
+    i8_write_as<T, 1>(c, sum, lds, wave, m0, m_end, n0, lane);
+  else
+    i8_write_as<T, 2>(c, sum, lds, wave, m0, m_end, n0, lane);
+}
+
+namespace {
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool DIRECT>
+hipError_t launch_tile(const I8Call& c, hipStream_t s) {
+  const int tiles_m = (int)i8_tiles_m(c, BM);
+  const int tiles_n = (int)((i8_b_rows(c) + BN - 1) / BN);
+  const I8TileArgs p{c, tiles_m, tiles_n, 8};
+  const dim3 grid((unsigned)tiles_m * tiles_n);
+  if (c.groups > 0) {
+    typedef I8Tile<BM, BN, WM, WN, STAGES, DIRECT, true> T;
+    i8_tile_kernel<T><<<grid, T::THREADS, 0, s>>>(p);
+  } else {
+    typedef I8Tile<BM, BN, WM, WN, STAGES, DIRECT, false> T;
+    i8_tile_kernel<T><<<grid, T::THREADS, 0, s>>>(p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool i8_direct(const I8Call& c) {
+  // 32-bit byte offsets from a tile's first row (from A's where rows are read by index,
+  // over both halves of B with a gate).
+  const int64_t a_rows = c.index != nullptr ? c.a_rows : 256;
+  const int64_t b_rows = 256 + (c.gated ? (int64_t)c.N : 0);
+  return c.lda % 16 == 0 && c.ldb % 16 == 0 && (reinterpret_cast<uintptr_t>(c.A) & 15u) == 0 &&
+         (reinterpret_cast<uintptr_t>(c.B) & 15u) == 0 && a_rows * c.lda < (1ll << 32) &&
+         b_rows * c.ldb < (1ll << 32);
+}
+
+hipError_t launch_i8_tile(const I8Call& c, int tile, hipStream_t s) {
+  switch (tile) {
+    case 0: return launch_tile<256, 256, 2, 4, 2, true>(c, s);
+    case 1: return launch_tile<128, 128, 2, 2, 2, true>(c, s);
+    case 2: return launch_tile<64, 64, 2, 2, 4, true>(c, s);
+    default: return launch_tile<128, 128, 2, 2, 2, false>(c, s);
+  }
+}
+
+}  // namespace lasg

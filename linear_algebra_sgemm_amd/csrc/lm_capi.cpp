@@ -1,6 +1,6 @@
-// C ABI of the 8-bit operators and the mixture-of-experts layer (declared in
-// include/gemm.h): argument checks, quick returns, and the launch.  None of
-// these calls allocates, copies to the host or uses the library's own
+// C ABI of the 8-bit operators, the mixture-of-experts layer and the exchange of
+// tokens with the experts' order (declared in include/gemm.h): argument checks,
+// quick returns, and the launch.  None of these calls allocates, copies to the host or uses the library's own
 // workspace, so all may be captured into a graph and run on any stream.
 #include <atomic>
 
@@ -10,6 +10,12 @@
 namespace {
 
 std::atomic<int> g_force_moe_rows{0};
+std::atomic<int> g_force_i8_tile{-1};
+
+constexpr int kMaxI8K = 131071;         // 2^14 K stays below 2^31
+constexpr int kMaxI8Cols = 1 << 20;     // of a row that i8_quantize takes
+constexpr int kMaxExperts = 1024, kMaxTopK = 32;
+constexpr int64_t kMaxEntries = 1 << 30;   // of a sort
 
 bool ld_ok(int ld, int cols) { return ld >= (cols > 1 ? cols : 1); }
 int blocks(int n) { return (int)(((int64_t)n + 127) / 128); }
@@ -117,6 +123,159 @@ int moe_ffn(const moe_shape_t* shape, const uint16_t* X, int ldx, const uint16_t
   if (s.tokens == 0) return GEMM_STATUS_SUCCESS;
   const lasg::MoeCall c{s, X, ldx, R, ldr, W1, ld1, S1, W2, ld2, S2, ids, w, Y, ldy, workspace};
   return finish(lasg::launch_moe(c, lasg::library_cus(), g_force_moe_rows.load(), stream));
+}
+
+int i8_quantize(int rows, int cols, int type, const void* X, int ldx, int8_t* Q, int ldq, float* S,
+                hipStream_t stream) {
+  if (rows < 0 || cols < 0 || cols > kMaxI8Cols || !float_type(type) || !ld_ok(ldx, cols) ||
+      !ld_ok(ldq, cols))
+    return GEMM_STATUS_INVALID_VALUE;
+  const bool empty = rows == 0 || cols == 0;
+  if (!empty && (X == nullptr || Q == nullptr || S == nullptr)) return GEMM_STATUS_INVALID_VALUE;
+  if (!aligned(X, elem(type)) || !aligned(S, 4)) return GEMM_STATUS_INVALID_VALUE;
+  if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
+  if (empty) return GEMM_STATUS_SUCCESS;
+  const lasg::I8QuantizeCall c{rows, cols, type, X, ldx, Q, ldq, S};
+  return finish(lasg::launch_i8_quantize(c, lasg::library_cus(), stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Both forms of the int8 product; groups 0: no groups.
+int i8_product(bool grouped, int groups, const int* offsets, int M, int N, int K, float alpha,
+               const int8_t* A, int lda, const float* SA, int a_rows, const int* index, int per,
+               const int8_t* B, int ldb, const float* SB, const float* bias, int act, int gated,
+               int type, void* C, int ldc, hipStream_t stream) {
+  if (M < 0 || N < 0 || K < 0 || K > kMaxI8K) return GEMM_STATUS_INVALID_VALUE;
+  if (!ld_ok(lda, K) || !ld_ok(ldb, K) || !ld_ok(ldc, N)) return GEMM_STATUS_INVALID_VALUE;
+  if (!act_ok(act) || !float_type(type) || !flag_ok(gated)) return GEMM_STATUS_INVALID_VALUE;
+  if (gated && N > (1 << 30)) return GEMM_STATUS_INVALID_VALUE;
+  if (grouped) {
+    if (groups < 0 || groups > kMaxExperts || per < 1 || a_rows < 0)
+      return GEMM_STATUS_INVALID_VALUE;
+    if (index == nullptr && a_rows < M) return GEMM_STATUS_INVALID_VALUE;
+  }
+  const bool empty = M == 0 || N == 0 || (grouped && groups == 0);
+  const bool reads_ab = !empty && K > 0 && alpha != 0.0f;
+  if (!empty && (C == nullptr || (grouped && offsets == nullptr))) return GEMM_STATUS_INVALID_VALUE;
+  if (reads_ab && (A == nullptr || B == nullptr || SA == nullptr || SB == nullptr || a_rows == 0))
+    return GEMM_STATUS_INVALID_VALUE;
+  if (!aligned(C, elem(type)) || !aligned(SA, 4) || !aligned(SB, 4) || !aligned(bias, 4) ||
+      !aligned(offsets, 4) || !aligned(index, 4))
+    return GEMM_STATUS_INVALID_VALUE;
+  if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
+  if (empty) return GEMM_STATUS_SUCCESS;
+  const lasg::I8Call c{M, N, reads_ab ? K : 0, alpha, A, lda, SA, reads_ab ? index : nullptr, a_rows,
+                       per, B, ldb, SB, bias, act, gated, type, C, ldc, groups, offsets};
+  return finish(lasg::launch_i8_gemm(c, lasg::library_cus(), g_force_i8_tile.load(), stream));
+}
+
+// What the three calls that go token by token share; `rows`: of the sorted array.
+bool exchange_ok(int tokens, int top_k, int cols, int type, int rows, const int* pos, const float* w) {
+  return tokens >= 0 && top_k >= 1 && top_k <= kMaxTopK && cols >= 0 && float_type(type) &&
+         rows >= 0 && aligned(pos, 4) && aligned(w, 4) &&
+         (tokens == 0 || cols == 0 || pos != nullptr);
+}
+
+}  // namespace
+
+extern "C" {
+
+int i8_gemm_bias_act(int M, int N, int K, float alpha, const int8_t* A, int lda, const float* SA,
+                     const int8_t* B, int ldb, const float* SB, const float* bias, int act, int gated,
+                     int type, void* C, int ldc, hipStream_t stream) {
+  return i8_product(false, 0, nullptr, M, N, K, alpha, A, lda, SA, M, nullptr, 1, B, ldb, SB, bias,
+                    act, gated, type, C, ldc, stream);
+}
+
+int i8_gemm_grouped(int groups, const int* offsets, int M, int N, int K, float alpha, const int8_t* A,
+                    int lda, const float* SA, int a_rows, const int* index, int per, const int8_t* B,
+                    int ldb, const float* SB, const float* bias, int act, int gated, int type, void* C,
+                    int ldc, hipStream_t stream) {
+  return i8_product(true, groups, offsets, M, N, K, alpha, A, lda, SA, a_rows, index, per, B, ldb, SB,
+                    bias, act, gated, type, C, ldc, stream);
+}
+
+int moe_sort_workspace(int tokens, int top_k, int experts, size_t* bytes) {
+  if (tokens < 0 || top_k < 1 || top_k > kMaxTopK || experts < 1 || experts > kMaxExperts ||
+      (int64_t)tokens * top_k > kMaxEntries || bytes == nullptr)
+    return GEMM_STATUS_INVALID_VALUE;
+  *bytes = lasg::sort_workspace_bytes((int64_t)tokens * top_k, experts);
+  return GEMM_STATUS_SUCCESS;
+}
+
+int moe_sort(int tokens, int top_k, int experts, const int* ids, int* offsets, int* src, int* pos,
+             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  size_t need = 0;
+  if (moe_sort_workspace(tokens, top_k, experts, &need) != GEMM_STATUS_SUCCESS ||
+      offsets == nullptr)
+    return GEMM_STATUS_INVALID_VALUE;
+  if (tokens > 0 && (ids == nullptr || src == nullptr || pos == nullptr || workspace == nullptr ||
+                     workspace_bytes < need))
+    return GEMM_STATUS_INVALID_VALUE;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(src, 4) || !aligned(pos, 4) ||
+      !aligned(workspace, 256))
+    return GEMM_STATUS_INVALID_VALUE;
+  if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
+  const lasg::SortCall c{tokens * top_k, experts, ids, offsets, src, pos, workspace};
+  return finish(lasg::launch_sort(c, stream));
+}
+
+int moe_dispatch(int tokens, int top_k, int cols, int type, const void* X, int ldx, const int* pos,
+                 const float* w, void* Y, int ldy, int y_rows, hipStream_t stream) {
+  if (!exchange_ok(tokens, top_k, cols, type, y_rows, pos, w) || !ld_ok(ldx, cols) ||
+      !ld_ok(ldy, cols) || !aligned(X, elem(type)) || !aligned(Y, elem(type)))
+    return GEMM_STATUS_INVALID_VALUE;
+  const bool empty = tokens == 0 || cols == 0 || y_rows == 0;
+  if (!empty && (X == nullptr || Y == nullptr)) return GEMM_STATUS_INVALID_VALUE;
+  if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
+  if (empty) return GEMM_STATUS_SUCCESS;
+  const lasg::ExchangeCall c{tokens, top_k, cols, type, X, ldx, nullptr, 0, y_rows, pos, w, Y, ldy,
+                             nullptr};
+  return finish(lasg::launch_dispatch(c, stream));
+}
+
+int moe_combine(int tokens, int top_k, int cols, int type, const void* X, int ldx, int x_rows,
+                const int* pos, const float* w, void* Y, int ldy, hipStream_t stream) {
+  if (!exchange_ok(tokens, top_k, cols, type, x_rows, pos, w) || !ld_ok(ldx, cols) ||
+      !ld_ok(ldy, cols) || !aligned(X, elem(type)) || !aligned(Y, elem(type)))
+    return GEMM_STATUS_INVALID_VALUE;
+  const bool empty = tokens == 0 || cols == 0;
+  if (!empty && ((X == nullptr && x_rows > 0) || Y == nullptr)) return GEMM_STATUS_INVALID_VALUE;
+  if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
+  if (empty) return GEMM_STATUS_SUCCESS;
+  const lasg::ExchangeCall c{tokens, top_k, cols, type, nullptr, 0, X, ldx, x_rows, pos, w, Y, ldy,
+                             nullptr};
+  return finish(lasg::launch_combine(c, stream));
+}
+
+int moe_combine_grad(int tokens, int top_k, int cols, int type, const void* dY, int lddy,
+                     const void* X, int ldx, int x_rows, const int* pos, const float* w, void* dX,
+                     int lddx, float* dw, hipStream_t stream) {
+  if (!exchange_ok(tokens, top_k, cols, type, x_rows, pos, w) || !ld_ok(lddy, cols) ||
+      !aligned(dY, elem(type)) || !aligned(X, elem(type)) || !aligned(dX, elem(type)) ||
+      !aligned(dw, 4))
+    return GEMM_STATUS_INVALID_VALUE;
+  if ((dw != nullptr && !ld_ok(ldx, cols)) || (dX != nullptr && !ld_ok(lddx, cols)))
+    return GEMM_STATUS_INVALID_VALUE;
+  if (tokens > 0 && dX == nullptr && dw == nullptr) return GEMM_STATUS_INVALID_VALUE;
+  if (tokens > 0 && pos == nullptr) return GEMM_STATUS_INVALID_VALUE;
+  const bool rows = tokens > 0 && cols > 0 && x_rows > 0;
+  if (rows && (dY == nullptr || (dw != nullptr && X == nullptr))) return GEMM_STATUS_INVALID_VALUE;
+  if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
+  // (Without columns dw is all zeros still.)
+  if (tokens == 0 || (cols == 0 && dw == nullptr)) return GEMM_STATUS_SUCCESS;
+  const lasg::ExchangeCall c{tokens, top_k, cols, type, dY, lddy, X, ldx, rows ? x_rows : 0, pos, w,
+                             dX, lddx, dw};
+  return finish(lasg::launch_combine_grad(c, stream));
+}
+
+int gemm_debug_force_i8_tile(int tile) {
+  if (tile < -1 || tile >= lasg::kI8TileCount) return GEMM_STATUS_INVALID_VALUE;
+  g_force_i8_tile.store(tile);
+  return GEMM_STATUS_SUCCESS;
 }
 
 int gemm_debug_force_moe_rows(int rows) {

@@ -86,4 +86,70 @@ size_t moe_workspace_bytes(const moe_shape_t& s);
 // `force_rows`: rows of a weight per workgroup, 0 = by shape.
 hipError_t launch_moe(const MoeCall& c, int cus, int force_rows, hipStream_t s);
 
+struct I8QuantizeCall {
+  int rows, cols, type;
+  const void* X;
+  int ldx;
+  int8_t* Q;
+  int ldq;
+  float* S;
+};
+hipError_t launch_i8_quantize(const I8QuantizeCall& c, int cus, hipStream_t s);
+
+struct I8Call {
+  int M, N, K;      // K == 0: the sums are zero; A, B and their scales are not read
+  float alpha;
+  const int8_t* A;
+  int lda;
+  const float* SA;
+  const int* index; // null, or row r of the product reads row index[r] / per of A
+  int a_rows, per;
+  const int8_t* B;  // a group's matrix behind the other, SB and bias likewise
+  int ldb;
+  const float* SB;
+  const float* bias;
+  int act, gated;
+  int type;         // of C
+  void* C;
+  int ldc;
+  int groups;       // 0: one product of all rows
+  const int* offsets;
+};
+// Output tile: 0 = 256 x 256, 1 = 128 x 128, 2 = 64 x 64 copied straight into LDS; 3 =
+// 128 x 128 through registers; with K split over a workgroup's waves 4 = 64 x 32, 5 = 64 x 16,
+// 6 = 32 x 32, 7 = 32 x 16, 8 = 16 x 32, 9 = 16 x 16.  (Columns are rows of B: half as many of C
+// with a gate.)
+constexpr int kI8TileCount = 10;
+int i8_tile(const I8Call& c, int cus, int force);
+hipError_t launch_i8_gemm(const I8Call& c, int cus, int force, hipStream_t s);
+
+// Tokens in the experts' order and back (exchange_kernels.hip).
+struct SortCall {
+  int entries, experts;
+  const int* ids;
+  int* offsets;
+  int* src;
+  int* pos;
+  void* ws;
+};
+size_t sort_workspace_bytes(int64_t entries, int experts);
+hipError_t launch_sort(const SortCall& c, hipStream_t s);
+
+struct ExchangeCall {
+  int tokens, top_k, cols, type;
+  const void* tok;      // one row a token (dispatch's X, the gradient's dY); null for combine
+  int ldtok;
+  const void* sorted;   // one row a (token, slot), in the experts' order; null for dispatch
+  int ldsorted;
+  int rows;             // of the sorted arrays
+  const int* pos;
+  const float* w;       // null: ones
+  void* out;            // dispatch's and the gradient's sorted rows, combine's tokens
+  int ldout;
+  float* dw;            // the gradient's
+};
+hipError_t launch_dispatch(const ExchangeCall& c, hipStream_t s);
+hipError_t launch_combine(const ExchangeCall& c, hipStream_t s);
+hipError_t launch_combine_grad(const ExchangeCall& c, hipStream_t s);
+
 }  // namespace lasg
