@@ -51,10 +51,10 @@ int gemm_debug_force_tile(int op, int tile);
 
 /*
  * Force the tile of later calls of i8_gemm_bias_act and i8_gemm_grouped: -1 = by
- * shape (the default); 0 = 256 x 256, 1 = 128 x 128 and 2 = 64 x 64 rows of A and B, copied straight
- * into LDS (where rows are off 16-byte boundaries, 3); 3 = 128 x 128 through registers; and
- * tiles whose eight waves split K between them: 4 = 64 x 32, 5 = 64 x 16, 6 = 32 x 32, 7 =
- * 32 x 16, 8 = 16 x 32, 9 = 16 x 16.  Returns GEMM_STATUS_INVALID_VALUE for another number.
+ * shape (the default); 0 = 256 x 256, 1 = 128 x 256, 2 = 128 x 128, 3 = 64 x 128, 4 = 64 x 64 and
+ * 5 = 32 x 128 rows of A and B, copied straight into LDS (where rows are off 16-byte boundaries,
+ * 6); 6 = 128 x 128 through registers; and tiles whose eight waves split K between them:
+ * 7 = 64 x 32, 8 = 32 x 32, 9 = 32 x 16, 10 = 16 x 32, 11 = 16 x 16.  Returns GEMM_STATUS_INVALID_VALUE for another number.
  * Pure host state, not synchronised with calls in flight on other threads.
  */
 int gemm_debug_force_i8_tile(int tile);

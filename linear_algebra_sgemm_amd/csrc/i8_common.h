@@ -9,7 +9,7 @@ namespace lasg {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-// The tiled kernels (i8_tile_kernels.hip): tiles 0 to 3 of i8_tile.  Tiles 0 to 2
+// The tiled kernels (i8_tile_kernels.hip): tiles 0 to 6 of i8_tile.  Tiles 0 to 5
 // copy straight into LDS, which the call has to allow (i8_direct).
 bool i8_direct(const I8Call& c);
 hipError_t launch_i8_tile(const I8Call& c, int tile, hipStream_t s);

@@ -248,22 +248,44 @@ hipError_t launch_ksplit(const I8Call& c, hipStream_t s) {
 
 }  // namespace
 
-// The rule takes the tile of the least estimated time.
+// The rule takes the tile of the least estimated time.  Measured on 256 CUs:
+//  * tiles through LDS take a time per block of K that depends on how many of them
+//    run, not on the shape: kTiles has it in ns for one of them, for one on every CU and for as
+//    many as fit a CU.  4096 x 4096 x 4096: 256 x 256 62 us, 128 x 256 65, 128 x 128 73; 4096 x 14336 x
+//    4096, 3.5 rounds of either: 241 and 228; 1024 x 4096 x 4096: 128 x 128 26, 128 x 256 33; 1024
+//    x 1024 x 4096: 64 x 64 11.1, 64 x 128 14.8, 128 x 128 23.9.
+//  * where the weights bound a call it takes their bytes at 5.5 TB/s, and the bytes that the
+//    CUs load at 40: 4 tokens on 64 experts of 2048 x 4096 32 x 128 tiles 41 us, 64 x 64 45; 64 rows
+//    by 28672 x 4096 64 x 128 25, 64 x 64 28, 32 x 128 30.
+//  * K-split tiles of m x n take (m + n) K bytes through a CU's load path at 23 bytes a ns: 1 x
+//    4096 x 4096 16 x 16 6.4 us, 64 x 64 through LDS 10.6; off 16-byte boundaries about 2.5 times
+//    that (128 x 4096 x 4095: 64 x 32 52 us, 32 x 32 67, 128 x 128 through registers 88).
 int i8_tile(const I8Call& c, int cus, int force) {
-  const int64_t b_rows = i8_b_rows(c);
-  // Rows a group: as if they were evenly spread.
-  const int64_t groups = c.groups > 0 ? (c.groups < c.M ? c.groups : c.M) : 1;
-  const int64_t rows = (c.M + groups - 1) / groups;
-  const auto tiles = [&](int m, int n) {
-    return groups * ((rows + m - 1) / m) * ((b_rows + n - 1) / n);
+  struct Tile {
+    int m, n, per_cu;
+    double one, every, all;
   };
+  static const Tile kTiles[7] = {{256, 256, 1, 1250, 1840, 1840}, {128, 256, 2, 970, 1140, 1910},
+                                 {128, 128, 2, 700, 760, 1130},   {64, 128, 2, 440, 470, 750},
+                                 {64, 64, 2, 320, 330, 480},      {32, 128, 2, 350, 360, 540},
+                                 {128, 128, 2, 2600, 2600, 2700}};
+  static const int kSplit[5][2] = {{64, 32}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
+  const int64_t b_rows = i8_b_rows(c);
   // 32-bit row, column and tile numbers in the tiled kernels.
   const bool tiled = c.M <= (1 << 30) && b_rows <= (1 << 30) &&
-                     i8_tiles_m(c, 64) * ((b_rows + 63) / 64) < (1 << 23);
+                     i8_tiles_m(c, 32) * ((b_rows + 63) / 64) < (1 << 23);
   const bool direct = i8_direct(c);
-  static const int kSplit[6][2] = {{64, 32}, {64, 16}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
   int tile = force;
   if (tile < 0) {
+    // Groups with rows, and rows of such a group, as if they were spread at random.
+    const double rows = c.M, groups = c.groups > 0 ? c.groups : 1;
+    const double active = c.groups > 0 ? groups * (1 - __builtin_exp(-rows / groups)) : 1;
+    const double each = rows / active;
+    const auto tiles = [&](int m, int n) {
+      const double down = c.groups == 0 ? __builtin_ceil(rows / m) : each <= 0.7 * m ? 1 : each / m + 0.5;
+      return active * down * (double)((b_rows + n - 1) / n);
+    };
+    const double weights = active * (double)b_rows * c.K;
     double best = 1e30;
     const auto offer = [&](int t, double cost) {
       if (cost < best) {
@@ -271,43 +293,38 @@ int i8_tile(const I8Call& c, int cus, int force) {
         tile = t;
       }
     };
-    if (tiled) {
-      // (start and end count as two blocks)
-      const double blocks = (double)(((int64_t)c.K + kBlockK - 1) / kBlockK) + 2;
-      const auto ring = [&](int m, int n, double one, double two) {
-        const double per_cu = (double)tiles(m, n) / cus;
-        return blocks * (per_cu <= 1 ? one : per_cu <= 2 ? two : two * per_cu / 2);
-      };
-      const double t128 = ring(128, 128, 700, 900);
-      if (direct) {
-        const double per_cu = (double)((tiles(256, 256) + cus - 1) / cus);
-        offer(0, blocks * 1500 * per_cu);
-        offer(1, t128);
-        offer(2, ring(64, 64, 500, 550));
-      } else {
-        offer(3, 2 * t128);
-      }
+    for (int t = direct ? 0 : 6; tiled && t < (direct ? 6 : 7); ++t) {
+      const Tile& x = kTiles[t];
+      const double n = tiles(x.m, x.n), round = (double)x.per_cu * cus;
+      const double full = __builtin_floor(n / round), left = n - full * round, on = left / cus;
+      double last = on <= 1 ? x.one + on * (x.every - x.one) : x.every + (on - 1) * (x.all - x.every);
+      if (left == 0) last = 0;
+      // (after whole rounds a CU's only workgroup gains little from the others' absence)
+      else if (full > 0 && x.per_cu == 1 && last < 0.85 * x.all) last = 0.85 * x.all;
+      const double blocks = (double)((c.K + kBlockK - 1) / kBlockK) + 2;   // (2: start and end)
+      const double work = blocks * (full * x.all + last);
+      const double bytes = weights / 5500 + n * (x.m + x.n) * c.K / 40000;
+      offer(t, work > bytes ? work : bytes);
     }
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < 5; ++i) {
       const int m = kSplit[i][0], n = kSplit[i][1];
-      const double rounds = (double)((tiles(m, n) + cus - 1) / cus);
-      offer(4 + i, rounds * (m + n) * ((double)c.K + 512) / 23);
+      const double rounds = __builtin_ceil(tiles(m, n) / cus);
+      offer(7 + i, rounds * (m + n) * ((double)c.K + 512) / (direct ? 23 : 9));
     }
   }
-  if (tile < 4 && !tiled) tile = 4;
-  if (tile < 3 && !direct) tile = 3;
+  if (tile < 7 && !tiled) tile = 7;
+  if (tile < 6 && !direct) tile = 6;
   return tile;
 }
 
 hipError_t launch_i8_gemm(const I8Call& c, int cus, int force, hipStream_t s) {
   const int tile = i8_tile(c, cus, force);
   switch (tile) {
-    case 4: return launch_ksplit<4, 2>(c, s);
-    case 5: return launch_ksplit<4, 1>(c, s);
-    case 6: return launch_ksplit<2, 2>(c, s);
-    case 7: return launch_ksplit<2, 1>(c, s);
-    case 8: return launch_ksplit<1, 2>(c, s);
-    case 9: return launch_ksplit<1, 1>(c, s);
+    case 7: return launch_ksplit<4, 2>(c, s);
+    case 8: return launch_ksplit<2, 2>(c, s);
+    case 9: return launch_ksplit<2, 1>(c, s);
+    case 10: return launch_ksplit<1, 2>(c, s);
+    case 11: return launch_ksplit<1, 1>(c, s);
     default: return launch_i8_tile(c, tile, s);
   }
 }

@@ -21,7 +21,8 @@
 
 namespace lasg {
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, bool DIRECT_, bool GROUPED_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, bool DIRECT_, bool OWN_B_,
+          bool GROUPED_>
 struct I8Tile {
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr int STAGES = STAGES_;
@@ -29,15 +30,20 @@ struct I8Tile {
   static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = WAVES * kWave;
   static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
   static constexpr int FM = WTM / 32, FN = WTN / 32, BLOCKS = FM * FN;
-  static constexpr int A_BYTES = BM * kBlockK, STAGE_BYTES = (BM + BN) * kBlockK;
+  // Waves side by side only: each copies and reads its own rows of B, so one stage of B
+  // is enough (refilled once the wave holds its fragments).
+  static constexpr bool OWN_B = OWN_B_;
+  static_assert(!OWN_B || (WAVES_M == 1 && STAGES == 2 && DIRECT), "waves side by side");
+  static constexpr int A_BYTES = BM * kBlockK, B_BYTES = BN * kBlockK;
+  static constexpr int B_AT = STAGES * A_BYTES;
+  static constexpr int STAGES_BYTES = B_AT + (OWN_B ? 1 : STAGES) * B_BYTES;
   static constexpr int A_LOADS = BM / 8 / WAVES, B_LOADS = BN / 8 / WAVES;   // per wave, 1 KiB each
   static constexpr int LOADS = A_LOADS + B_LOADS;
   // Epilogue: 32 rows of each wave's results, then the scales (split) and bias.
   static constexpr int REGION = 32 * WTN * 4;
   static constexpr int SCALES_AT = WAVES * REGION;
   static constexpr int EPILOGUE_BYTES = SCALES_AT + 4 * (3 * BN + 2 * BM);
-  static constexpr int LDS_BYTES =
-      STAGES * STAGE_BYTES > EPILOGUE_BYTES ? STAGES * STAGE_BYTES : EPILOGUE_BYTES;
+  static constexpr int LDS_BYTES = STAGES_BYTES > EPILOGUE_BYTES ? STAGES_BYTES : EPILOGUE_BYTES;
   static_assert(DIRECT || STAGES == 2, "through registers one tile ahead");
   static_assert(STAGES >= 2 && (STAGES - 1) * LOADS <= 63, "copies on their way must fit vmcnt");
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "copies split evenly over waves");
@@ -48,6 +54,10 @@ struct I8Tile {
 struct I8TileArgs {
   I8Call c;
   int tiles_m, tiles_n, group_m;
+  // K tiles that the tiles of one group (of a tile column) start behind those of the one
+  // before.  All at the same K would read addresses a row apart, a power of two in most
+  // weights, from a part of the memory channels only.
+  int group_step, column_step;
 };
 
 namespace {
@@ -207,16 +217,21 @@ i8_tile_kernel(I8TileArgs p) {
     chunk = (l % 8) ^ ((row >> 1) & 7);
   };
   auto slot_at = [&](int v, int t) __attribute__((always_inline)) {
-    return t % T::STAGES * T::STAGE_BYTES +
-           (v < T::A_LOADS ? (wave * T::A_LOADS + v) * 1024
-                           : T::A_BYTES + (wave * T::B_LOADS + v - T::A_LOADS) * 1024);
+    return v < T::A_LOADS ? t % T::STAGES * T::A_BYTES + (wave * T::A_LOADS + v) * 1024
+                          : T::B_AT + (T::OWN_B ? 0 : t % T::STAGES * T::B_BYTES) +
+                                (wave * T::B_LOADS + v - T::A_LOADS) * 1024;
   };
   // K tiles in the order they are taken.  A last, shorter one goes through registers, with zeros
   // behind it; where whole ones are copied straight into LDS it is taken first, so that its
   // latency falls together with the first copies'.
   const bool tail_first = T::DIRECT && c.K % kBlockK != 0;
+  const int whole = tail_first ? kts - 1 : kts;
+  const int rotated = whole == 0 ? 0 : (int)(((unsigned)tile_n * p.column_step +
+                                              (unsigned)group * p.group_step) % (unsigned)whole);
   auto block_of = [&](int t) __attribute__((always_inline)) {
-    return !tail_first ? t : t == 0 ? kts - 1 : t - 1;
+    if (tail_first && t == 0) return whole;
+    const int x = t - (tail_first ? 1 : 0) + rotated;
+    return x < whole ? x : x - whole;
   };
   uint32_t off[T::DIRECT ? T::LOADS : 1];
   if constexpr (T::DIRECT) {
@@ -233,20 +248,35 @@ i8_tile_kernel(I8TileArgs p) {
                   lds_base + slot_at(v, t));
   };
   // K tile t through registers, any alignment: loaded, and later stored.
-  u32x4 held[T::DIRECT ? 1 : T::LOADS];
-  auto load_one = [&](int t, int v) __attribute__((always_inline)) {
-    int row, chunk;
-    slot(v, lane, row, chunk);
-    const int8_t* at = v < T::A_LOADS ? a_tile + a_row(row) * c.lda
-                                      : b_tile + (int64_t)b_row(row) * c.ldb;
-    const int k = block_of(t) * kBlockK + 16 * chunk;
-    return block_of(t) * kBlockK + kBlockK <= c.K ? load16(at + k) : load16_row(at, k, c.K);
+  u32x4 held[T::LOADS];
+  auto load_tile = [&](int t) __attribute__((always_inline)) {
+    const int k0 = block_of(t) * kBlockK;
+#pragma unroll
+    for (int v = 0; v < T::LOADS; ++v) {
+      int row, chunk;
+      slot(v, lane, row, chunk);
+      const int8_t* at = v < T::A_LOADS ? a_tile + a_row(row) * c.lda
+                                        : b_tile + (int64_t)b_row(row) * c.ldb;
+      const int k = k0 + 16 * chunk;
+      held[v] = k0 + kBlockK <= c.K ? load16(at + k) : load16_row(at, k, c.K);
+    }
   };
-  auto copy_by_hand = [&](int t) __attribute__((always_inline)) {
-#pragma unroll 1
+  auto store_tile = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
     for (int v = 0; v < T::LOADS; ++v)
-      *reinterpret_cast<u32x4*>(lds + slot_at(v, t) + 16 * lane) = load_one(t, v);
+      *reinterpret_cast<u32x4*>(lds + slot_at(v, t) + 16 * lane) = held[v];
   };
+
+  // The scales and bias that the epilogue will need, one row of the tile a thread.
+  static_assert(T::THREADS >= T::BM && T::THREADS >= T::BN, "a thread for every row");
+  float sa = 0.0f, sb = 0.0f, bias = 0.0f;
+  if ((int)threadIdx.x < T::BN) {
+    const int64_t n = group_b + n0 + b_row(threadIdx.x);
+    if (c.K != 0) sb = c.SB[n];
+    if (c.bias != nullptr) bias = c.bias[n];
+  }
+  if ((int)threadIdx.x < T::BM && c.K != 0)
+    sa = c.SA[a_row(threadIdx.x) + (c.index != nullptr ? 0 : m0)];
 
   i32x16 sum[T::FM][T::FN];
 #pragma unroll
@@ -257,15 +287,20 @@ i8_tile_kernel(I8TileArgs p) {
   // This lane's chunk of a fragment row in step s is (2 s + half) permuted.
   const uint32_t swizzled = 16 * (half ^ ((l32 >> 1) & 7));
   const uint32_t a_frag = (wm * T::WTM + l32) * kBlockK;
-  const uint32_t b_frag = T::A_BYTES + (wn * T::WTN + l32) * kBlockK;
+  const uint32_t b_frag = T::B_AT + (wn * T::WTN + l32) * kBlockK;
+  auto read_a = [&](I8Frags<T>& f, int t, int s) __attribute__((always_inline)) {
+    const uint8_t* st = lds + t % T::STAGES * T::A_BYTES + (swizzled ^ (32 * s)) + a_frag;
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(st + i * 32 * kBlockK);
+  };
+  auto read_b = [&](I8Frags<T>& f, int t, int s) __attribute__((always_inline)) {
+    const uint8_t* st = lds + (T::OWN_B ? 0 : t % T::STAGES * T::B_BYTES) + (swizzled ^ (32 * s)) + b_frag;
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(st + j * 32 * kBlockK);
+  };
   auto read = [&](I8Frags<T>& f, int t, int s) __attribute__((always_inline)) {
-    const uint8_t* st = lds + t % T::STAGES * T::STAGE_BYTES + (swizzled ^ (32 * s));
-#pragma unroll
-    for (int i = 0; i < T::FM; ++i)
-      f.a[i] = *reinterpret_cast<const i32x4*>(st + a_frag + i * 32 * kBlockK);
-#pragma unroll
-    for (int j = 0; j < T::FN; ++j)
-      f.b[j] = *reinterpret_cast<const i32x4*>(st + b_frag + j * 32 * kBlockK);
+    read_a(f, t, s);
+    read_b(f, t, s);
   };
   auto multiply = [&](const I8Frags<T>& f, int x) __attribute__((always_inline)) {
     const int i = x / T::FN, j = x % T::FN;
@@ -279,10 +314,7 @@ i8_tile_kernel(I8TileArgs p) {
   auto k_tile = [&](int t, auto copy_next, auto more) __attribute__((always_inline)) {
     constexpr bool COPY = decltype(copy_next)::value, MORE = decltype(more)::value;
     read(f1, t, 1);
-    if constexpr (!T::DIRECT && MORE) {
-#pragma unroll
-      for (int v = 0; v < T::LOADS; ++v) held[v] = load_one(t + 1, v);
-    }
+    if constexpr (!T::DIRECT && MORE) load_tile(t + 1);
 #pragma unroll
     for (int x = 0; x < T::BLOCKS; ++x) multiply(f0, x);
     __builtin_amdgcn_sched_barrier(0);
@@ -294,11 +326,7 @@ i8_tile_kernel(I8TileArgs p) {
 #pragma unroll
     for (int x = 0; x < T::BLOCKS; ++x) multiply(f0, x);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (!T::DIRECT && MORE) {
-#pragma unroll
-      for (int v = 0; v < T::LOADS; ++v)
-        *reinterpret_cast<u32x4*>(lds + slot_at(v, t + 1) + 16 * lane) = held[v];
-    }
+    if constexpr (!T::DIRECT && MORE) store_tile(t + 1);
 #pragma unroll
     for (int x = 0; x < PRE; ++x) multiply(f1, x);
     if constexpr (MORE) {
@@ -326,13 +354,71 @@ i8_tile_kernel(I8TileArgs p) {
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  if (kts > 0) {
+  // The same for waves that own their rows of B: all of a K tile's fragments of B are
+  // read at its start, then their one stage takes the next tile's; one meeting, at the
+  // start.
+  auto k_tile_own = [&](int t, auto copy_next) __attribute__((always_inline)) {
+    constexpr bool COPY = decltype(copy_next)::value;
+    wait_vmcnt<0>();
+    lds_barrier();
+    I8Frags<T> b1, b2, b3;   // (their fragments of B only)
+    read_b(f0, t, 0);
+    read_a(f0, t, 0);
+    read_b(b1, t, 1);
+    read_b(b2, t, 2);
+    read_b(b3, t, 3);
+    // One step's products, with copies `first` .. `first` + `count` - 1 of the next tile between.
+    auto step = [&](const I8Frags<T>& a, const I8Frags<T>& b, int first, int count)
+        __attribute__((always_inline)) {
+#pragma unroll
+      for (int x = 0; x < T::BLOCKS; ++x) {
+        const int i = x / T::FN, j = x % T::FN;
+        sum[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b.b[j], a.a[i], sum[i][j], 0, 0, 0);
+        if constexpr (COPY) {
+#pragma unroll
+          for (int v = first + x * count / T::BLOCKS; v < first + (x + 1) * count / T::BLOCKS; ++v) {
+            __builtin_amdgcn_sched_barrier(0);
+            copy(t + 1, v);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    read_a(f1, t, 1);
+    step(f0, f0, 0, T::A_LOADS);
+    if constexpr (COPY) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // this wave's fragments of B are read
+    }
+    read_a(f0, t, 2);
+    step(f1, b1, T::A_LOADS, T::B_LOADS / 2);
+    read_a(f1, t, 3);
+    step(f0, b2, T::A_LOADS + T::B_LOADS / 2, T::B_LOADS - T::B_LOADS / 2);
+    step(f1, b3, 0, 0);
+  };
+
+  if constexpr (T::OWN_B) {
+    if (kts > 0) {
+      if (tail_first) {
+        load_tile(0);
+        store_tile(0);
+      } else {
+#pragma unroll
+        for (int v = 0; v < T::LOADS; ++v) copy(0, v);
+      }
+      int t = 0;
+      for (; t + 1 < kts; ++t) k_tile_own(t, std::true_type());
+      k_tile_own(t, std::false_type());
+    }
+  } else if (kts > 0) {
     if constexpr (T::DIRECT) {
 #pragma unroll
       for (int first = 0; first < T::STAGES; ++first) {
         if (first >= kts) break;
         if (first == 0 && tail_first) {
-          copy_by_hand(0);
+          load_tile(0);
+          store_tile(0);
         } else {
 #pragma unroll
           for (int v = 0; v < T::LOADS; ++v) copy(first, v);
@@ -343,7 +429,8 @@ i8_tile_kernel(I8TileArgs p) {
       else
         wait_vmcnt<0>();
     } else {
-      copy_by_hand(0);
+      load_tile(0);
+      store_tile(0);
     }
     lds_barrier();
     read(f0, 0, 0);
@@ -357,17 +444,16 @@ i8_tile_kernel(I8TileArgs p) {
   lds_barrier();   // every wave is done reading the stages
   {
     float* mb = reinterpret_cast<float*>(lds + T::SCALES_AT);
-    for (int x = threadIdx.x; x < T::BN; x += T::THREADS) {
-      const int64_t n = group_b + n0 + b_row(x);
-      const SplitScale s(c.K == 0 ? 0.0f : c.SB[n]);
+    float* ma = mb + 3 * T::BN;
+    const int x = threadIdx.x;
+    if (x < T::BN) {
+      const SplitScale s(sb);
       mb[x] = s.m;
       reinterpret_cast<int*>(mb)[T::BN + x] = s.e;
-      mb[2 * T::BN + x] = c.bias != nullptr ? c.bias[n] : 0.0f;
+      mb[2 * T::BN + x] = bias;
     }
-    float* ma = mb + 3 * T::BN;
-    for (int x = threadIdx.x; x < T::BM; x += T::THREADS) {
-      const int64_t a = a_row(x) + (c.index != nullptr ? 0 : m0);
-      const SplitScale s(c.K == 0 ? 0.0f : c.SA[a]);
+    if (x < T::BM) {
+      const SplitScale s(sa);
       ma[x] = s.m;
       reinterpret_cast<int*>(ma)[T::BM + x] = s.e;
     }
@@ -383,17 +469,22 @@ i8_tile_kernel(I8TileArgs p) {
 
 namespace {
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool DIRECT>
+template <int BM, int BN, int WM, int WN, int STAGES, bool DIRECT, bool OWN_B>
 hipError_t launch_tile(const I8Call& c, hipStream_t s) {
   const int tiles_m = (int)i8_tiles_m(c, BM);
   const int tiles_n = (int)((i8_b_rows(c) + BN - 1) / BN);
-  const I8TileArgs p{c, tiles_m, tiles_n, 8};
+  // Where the bytes of the weights bound the call (groups; few rows) different weights start at different K,
+  // the tiles that share them at the same: 512 tokens on 64 experts of 2048 x 4096 138 us
+  // without, 106 with; 64 rows by 28672 x 4096 31 and 27.  Many rows of one weight are 2 to 4 %
+  // slower with it, since tiles side by side then read A at different times.
+  const I8TileArgs p{c, tiles_m, tiles_n, c.groups > 0 ? 4 : 8, c.groups > 0 ? 11 : 0,
+                     c.groups == 0 && c.M <= 256 ? 11 : 0};
   const dim3 grid((unsigned)tiles_m * tiles_n);
   if (c.groups > 0) {
-    typedef I8Tile<BM, BN, WM, WN, STAGES, DIRECT, true> T;
+    typedef I8Tile<BM, BN, WM, WN, STAGES, DIRECT, OWN_B, true> T;
     i8_tile_kernel<T><<<grid, T::THREADS, 0, s>>>(p);
   } else {
-    typedef I8Tile<BM, BN, WM, WN, STAGES, DIRECT, false> T;
+    typedef I8Tile<BM, BN, WM, WN, STAGES, DIRECT, OWN_B, false> T;
     i8_tile_kernel<T><<<grid, T::THREADS, 0, s>>>(p);
   }
   return hipGetLastError();
@@ -413,10 +504,13 @@ bool i8_direct(const I8Call& c) {
 
 hipError_t launch_i8_tile(const I8Call& c, int tile, hipStream_t s) {
   switch (tile) {
-    case 0: return launch_tile<256, 256, 2, 4, 2, true>(c, s);
-    case 1: return launch_tile<128, 128, 2, 2, 2, true>(c, s);
-    case 2: return launch_tile<64, 64, 2, 2, 4, true>(c, s);
-    default: return launch_tile<128, 128, 2, 2, 2, false>(c, s);
+    case 0: return launch_tile<256, 256, 2, 4, 2, true, false>(c, s);
+    case 1: return launch_tile<128, 256, 1, 4, 2, true, true>(c, s);
+    case 2: return launch_tile<128, 128, 2, 2, 2, true, false>(c, s);
+    case 3: return launch_tile<64, 128, 2, 2, 3, true, false>(c, s);
+    case 4: return launch_tile<64, 64, 2, 2, 4, true, false>(c, s);
+    case 5: return launch_tile<32, 128, 1, 4, 4, true, false>(c, s);
+    default: return launch_tile<128, 128, 2, 2, 2, false, false>(c, s);
   }
 }
 

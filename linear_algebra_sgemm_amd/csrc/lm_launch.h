@@ -115,11 +115,11 @@ struct I8Call {
   int groups;       // 0: one product of all rows
   const int* offsets;
 };
-// Output tile: 0 = 256 x 256, 1 = 128 x 128, 2 = 64 x 64 copied straight into LDS; 3 =
-// 128 x 128 through registers; with K split over a workgroup's waves 4 = 64 x 32, 5 = 64 x 16,
-// 6 = 32 x 32, 7 = 32 x 16, 8 = 16 x 32, 9 = 16 x 16.  (Columns are rows of B: half as many of C
-// with a gate.)
-constexpr int kI8TileCount = 10;
+// Output tile: 0 = 256 x 256, 1 = 128 x 256, 2 = 128 x 128, 3 = 64 x 128, 4 = 64 x 64 and 5 =
+// 32 x 128 copied straight into LDS; 6 = 128 x 128 through registers; with K split over a
+// workgroup's waves 7 = 64 x 32, 8 = 32 x 32, 9 = 32 x 16, 10 = 16 x 32, 11 = 16 x 16.  (Columns are
+// rows of B: half as many of C with a gate.)
+constexpr int kI8TileCount = 12;
 int i8_tile(const I8Call& c, int cus, int force);
 hipError_t launch_i8_gemm(const I8Call& c, int cus, int force, hipStream_t s);
 

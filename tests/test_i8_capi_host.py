@@ -173,10 +173,10 @@ def test_exchange_accepts():
 
 
 def test_forced_tiles():
-    for tile in range(-1, 10):
+    for tile in range(-1, 12):
         assert lib.gemm_debug_force_i8_tile(tile) == lib.STATUS_SUCCESS
     assert lib.gemm_debug_force_i8_tile(-1) == lib.STATUS_SUCCESS
-    assert lib.gemm_debug_force_i8_tile(10) == BAD
+    assert lib.gemm_debug_force_i8_tile(12) == BAD
     assert lib.gemm_debug_force_i8_tile(-2) == BAD
 
 

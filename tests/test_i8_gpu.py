@@ -240,7 +240,7 @@ OPTIONS = [dict(), dict(type_="f32", act=2, gated=True), dict(type_="f16", act=1
            dict(type_="f16", act=0, gated=True, alpha=1.5), dict(act=2, bias=False)]
 
 
-@pytest.mark.parametrize("tile", range(-1, 10))
+@pytest.mark.parametrize("tile", range(-1, 12))
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 300, 128), (17, 33, 100), (64, 64, 64), (130, 250, 129),
                                    (33, 70, 1040), (257, 140, 2064), (300, 520, 777)])
 def test_product(M, N, K, tile):
@@ -252,13 +252,13 @@ def test_product(M, N, K, tile):
 
 
 @pytest.mark.parametrize("option", OPTIONS)
-@pytest.mark.parametrize("tile", range(-1, 10))
+@pytest.mark.parametrize("tile", range(-1, 12))
 def test_options(option, tile):
     note("i8 product options tile %d %s" % (tile, option))
     run(Product(70, 90, 400, pad=1, seed=3, **option), tile)
 
 
-@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 3, 4, 9])
+@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 4, 5, 6, 7, 11])
 def test_nothing_to_sum(tile):
     for K, alpha in ((0, 1.0), (40, 0.0)):
         note("i8 product K %d alpha %g tile %d" % (K, alpha, tile))
@@ -271,7 +271,7 @@ def test_nothing_to_sum(tile):
     run(p, tile)
 
 
-@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 3, 4, 9])
+@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 4, 5, 6, 7, 11])
 def test_longest_sums(tile):
     """131071 products of -128 and -128: 2^31 - 2^14 fits int32."""
     p = Product(3, 20, 131071, pad=1, type_="f32")
@@ -283,7 +283,7 @@ def test_longest_sums(tile):
     run(p, tile)
 
 
-@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 3, 4, 9])
+@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 4, 5, 6, 7, 11])
 def test_far_scales(tile):
     """Scales whose product with the sum stays in range though other orders of multiplying would not."""
     for ea, eb in ((110, -120), (-126, 100), (-126, 0), (120, -126), (-140, 100), (40, 60)):
@@ -294,7 +294,7 @@ def test_far_scales(tile):
         run(p, tile)
 
 
-@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 3, 4, 9])
+@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 4, 5, 6, 7, 11])
 def test_nan_scales(tile):
     p = Product(9, 40, 200, pad=1, type_="f32")
     for value in (float("nan"), float("inf")):
@@ -321,7 +321,7 @@ GROUPS = [
 ]
 
 
-@pytest.mark.parametrize("tile", range(-1, 10))
+@pytest.mark.parametrize("tile", range(-1, 12))
 @pytest.mark.parametrize("case", GROUPS, ids=lambda c: "%d-%d" % (c["M"], len(c["rows"])))
 def test_grouped(case, tile):
     n = case["M"] + tile
@@ -335,7 +335,7 @@ def test_grouped(case, tile):
 
 def test_bad_offsets_and_rows_stay_inside():
     """What the documentation leaves unspecified may come out anyhow, but only inside the arrays."""
-    for tile in range(-1, 10):
+    for tile in range(-1, 12):
         p = Product(40, 50, 100, rows=[10, 10, 10, 10], gather=7, per=2, pad=1)
         p.doffsets = torch.tensor([-5, 30, 12, 100000, 20], dtype=torch.int32, device="cuda")
         p.dindex = torch.tensor([-7, 2 ** 31 - 1, 3, -2 ** 31, 900] * 8, dtype=torch.int32, device="cuda")
@@ -348,7 +348,7 @@ def test_bad_offsets_and_rows_stay_inside():
         assert (c[40] == 77.0).all() and (c[:, 50:] == 77.0).all()
 
 
-@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 4, 9])
+@pytest.mark.parametrize("tile", [-1, 0, 1, 3, 5, 8, 11])
 def test_matrices_past_4_gib(tile):
     """The last group's matrix begins past 2^32 bytes; with an index so do rows of A."""
     groups, N, K = 9, 32768, 16384
