@@ -59,26 +59,20 @@ __device__ __forceinline__ int exclusive_sum(int x, int* part) {
   return before + sum - x;
 }
 
-// This wave's entries counted by expert into `count` (zeroed by all, before).
-__device__ __forceinline__ void count_wave(const SortCall& c, int64_t first, int n, int bits,
-                                           int* count) {
-  const int lane = threadIdx.x % kWave;
-  for (int at = 0; at < n; at += kWave) {
-    const int key = key_of(c, first + at + lane);
-    const uint64_t same = same_key(key, bits);
-    if (key < c.experts && __builtin_ctzll(same) == lane) count[key] += __popcll(same);
+// One entry a lane: its key, and the lanes of the wave with the same.
+struct Entry {
+  int key;
+  uint64_t same;
+  __device__ __forceinline__ Entry(const SortCall& c, int64_t i, int bits)
+      : key(key_of(c, i)), same(same_key(key, bits)) {}
+  // Counted by expert into the wave's own `count`.
+  __device__ __forceinline__ void count(const SortCall& c, int* count) const {
+    if (key < c.experts && __builtin_ctzll(same) == (int)threadIdx.x % kWave)
+      count[key] += __popcll(same);
   }
-}
-
-// The rows of this wave's entries; `next`: the next row of every expert for this wave.
-__device__ __forceinline__ void place_wave(const SortCall& c, int64_t first, int n, int bits,
-                                           int* next) {
-  const int lane = threadIdx.x % kWave;
-  for (int at = 0; at < n; at += kWave) {
-    const int64_t i = first + at + lane;
-    const int key = key_of(c, i);
-    const uint64_t same = same_key(key, bits);
-    const int rank = __popcll(same & ((1ull << lane) - 1));
+  // Its row; `next`: the next row of every expert for this wave.
+  __device__ __forceinline__ void place(const SortCall& c, int64_t i, int* next) const {
+    const int rank = __popcll(same & ((1ull << threadIdx.x % kWave) - 1));
     int row = -1;
     if (key < c.experts) row = next[key] + rank;
     if (i < c.entries) c.pos[i] = row;
@@ -87,7 +81,7 @@ __device__ __forceinline__ void place_wave(const SortCall& c, int64_t first, int
       if (rank == 0) next[key] = row + __popcll(same);
     }
   }
-}
+};
 
 __device__ __forceinline__ int bits_of(int experts) { return 32 - __builtin_clz(experts); }
 
@@ -102,7 +96,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs p) {
   __syncthreads();
   const int wave = threadIdx.x / kWave;
   const int64_t first = ((int64_t)blockIdx.x * kSortWaves + wave) * p.per_wave;
-  if (first < c.entries) count_wave(c, first, p.per_wave, bits_of(c.experts), count + wave * c.experts);
+  const int lane = threadIdx.x % kWave, bits = bits_of(c.experts);
+  for (int64_t i = first + lane; i < first + p.per_wave && i - lane < c.entries; i += kWave)
+    Entry(c, i, bits).count(c, count + wave * c.experts);
   __syncthreads();
   if ((int)threadIdx.x < c.experts) {
     int sum = 0;
@@ -120,7 +116,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs p) {
   for (int x = threadIdx.x; x < kSortWaves * c.experts; x += kSortThreads) next[x] = 0;
   __syncthreads();
   const int64_t first = ((int64_t)blockIdx.x * kSortWaves + wave) * p.per_wave;
-  if (first < c.entries) count_wave(c, first, p.per_wave, bits, next + wave * c.experts);
+  const int64_t mine = first + threadIdx.x % kWave, end = first + p.per_wave;
+  const Entry held(c, mine, bits);   // the first of a lane's entries, mostly the only one
+  held.count(c, next + wave * c.experts);
+  for (int64_t i = mine + kWave; i < end && i - mine + first < c.entries; i += kWave)
+    Entry(c, i, bits).count(c, next + wave * c.experts);
   // This expert's entries: of all chunks, and of those before this one.
   int total = 0, before = 0;
   if (p.chunks > 1 && e < c.experts) {
@@ -150,7 +150,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs p) {
   }
   if (blockIdx.x == 0 && e == 0) c.offsets[c.experts] = all;
   __syncthreads();
-  if (first < c.entries) place_wave(c, first, p.per_wave, bits, next + wave * c.experts);
+  held.place(c, mine, next + wave * c.experts);
+  for (int64_t i = mine + kWave; i < end && i - mine + first < c.entries; i += kWave)
+    Entry(c, i, bits).place(c, i, next + wave * c.experts);
   for (int64_t r = all + (int64_t)blockIdx.x * kSortThreads + threadIdx.x; r < c.entries;
        r += (int64_t)p.chunks * kSortThreads)
     c.src[r] = -1;
@@ -222,32 +224,42 @@ struct Row16<GEMM_TYPE_F32> {
   }
 };
 
+// How a call's rows lie: NARROW ones have fewer values than a piece and are stored one by one;
+// rows of WHOLE 128-byte lines are loaded past the caches where nobody else reads them
+// (combine of 4096 x 8 rows of 4096 bfloat16 56 -> 52 us; rows of 2050 values, whose
+// neighbours share lines, 31 -> 37).
+enum Rows { NARROW, ANY, WHOLE };
+
 // A thread's piece of a row: N values from column `col`.  The last piece of a row is its
 // last N values: those that it shares with the piece before come out the same there.
-// Rows of fewer values than a piece are handled one by one.
-template <int TYPE>
+template <int TYPE, Rows ROWS>
 struct Piece {
   typedef Row16<TYPE> R;
   int col;      // where it begins
-  int fresh;    // values at its front that the piece before has too
+  int shared;   // values at its front that the piece before has too
   bool inside;  // whether there is one
-  bool narrow;  // a row of fewer than N values
   __device__ __forceinline__ Piece(int at, int cols) {
     const int want = at * R::N;
     inside = want < cols;
-    narrow = cols < R::N;
-    col = narrow ? 0 : want < cols - R::N ? want : cols - R::N;
-    fresh = narrow || !inside ? 0 : want - col;
+    col = ROWS == NARROW ? 0 : want < cols - R::N ? want : cols - R::N;
+    shared = ROWS == NARROW || !inside ? 0 : want - col;
   }
+  // ONCE: nobody else reads this row.
+  template <bool ONCE = false>
   __device__ __forceinline__ u32x4 get(const void* base, int64_t row, int ld, int cols) const {
     const uint8_t* p = static_cast<const uint8_t*>(base) + row * ld * R::SIZE;
-    if (narrow) return load16_row(p, 0, cols * R::SIZE);
-    return load16(p + (int64_t)col * R::SIZE);
+    if constexpr (ROWS == NARROW) return load16_row(p, 0, cols * R::SIZE);
+    p += (int64_t)col * R::SIZE;
+    if constexpr (ONCE && ROWS == WHOLE)
+      return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+    return load16(p);
   }
+  // (Past the caches too: the rows of a long call do not fit them.  dispatch of 4096 x 8 rows
+  // of 4096 bfloat16 with its sort 63 -> 54 us.)
   __device__ __forceinline__ void put(void* base, int64_t row, int ld, int cols, u32x4 v) const {
     if (!inside) return;
     uint8_t* p = static_cast<uint8_t*>(base) + row * ld * R::SIZE;
-    if (narrow) {
+    if constexpr (ROWS == NARROW) {
 #pragma unroll
       for (int e = 0; e < R::N; ++e)
         if (e < cols) {
@@ -256,47 +268,61 @@ struct Piece {
           else
             reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(v[e / 2 % 4] >> (16 * (e & 1)));
         }
-      return;
+    } else {
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p + (int64_t)col * R::SIZE));
     }
-    *reinterpret_cast<u32x4_any*>(p + (int64_t)col * R::SIZE) = v;
   }
 };
 
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 512;   // at most
 constexpr int kSlots = 8;   // slots that are on their way together
 
 struct ExchangeArgs {
   ExchangeCall c;
-  int segments;   // workgroups of 256 pieces that a row takes
+  int segments;   // workgroups that a row takes, a piece a thread
   int64_t items;  // tokens x segments
 };
 
-// A slot's row, -1 for none (uniform over the workgroup).
-__device__ __forceinline__ int slot_row(const ExchangeCall& c, int64_t token, int slot) {
-  if (slot >= c.top_k) return -1;
-  const int r = c.pos[token * c.top_k + slot];
-  return r >= 0 && r < c.rows ? r : -1;
-}
+// The rows and weights of up to 64 slots of a token, a slot a lane: row -1 for none.  (Held
+// in scalar registers, those of eight slots spilled.)
+struct Slots {
+  int row;
+  float w;
+  __device__ __forceinline__ Slots(const ExchangeCall& c, int64_t token) {
+    const int slot = threadIdx.x % kWave;
+    const int64_t at = token * c.top_k + slot;
+    const int r = slot < c.top_k ? c.pos[at] : -1;
+    row = r >= 0 && r < c.rows ? r : -1;
+    w = row >= 0 && c.w != nullptr ? c.w[at] : 1.0f;
+  }
+  __device__ __forceinline__ int row_of(int slot) const {
+    return __builtin_amdgcn_readlane(row, slot);
+  }
+  __device__ __forceinline__ float weight_of(int slot) const {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), slot));
+  }
+};
 
 }  // namespace
 
-template <int TYPE>
+template <int TYPE, Rows ROWS>
 __global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(ExchangeArgs p) {
   typedef Row16<TYPE> R;
   const ExchangeCall& c = p.c;
   for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
     const int64_t token = item / p.segments;
     const int segment = (int)(item - token * p.segments);
-    const Piece<TYPE> piece(segment * kCopyThreads + threadIdx.x, c.cols);
+    const Piece<TYPE, ROWS> piece(segment * blockDim.x + threadIdx.x, c.cols);
+    const Slots slots(c, token);
     const u32x4 v = piece.get(c.tok, token, c.ldtok, c.cols);
     float x[R::N];
     R::wide(v, x);
     for (int slot = 0; slot < c.top_k; ++slot) {
-      const int row = slot_row(c, token, slot);
+      const int row = slots.row_of(slot);
       if (row < 0) continue;
       u32x4 out = v;
       if (c.w != nullptr) {
-        const float w = c.w[token * c.top_k + slot];
+        const float w = slots.weight_of(slot);
         float y[R::N];
 #pragma unroll
         for (int e = 0; e < R::N; ++e) y[e] = w * x[e];
@@ -307,27 +333,27 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(ExchangeArgs p) 
   }
 }
 
-template <int TYPE>
+template <int TYPE, Rows ROWS>
 __global__ void __launch_bounds__(kCopyThreads) combine_kernel(ExchangeArgs p) {
   typedef Row16<TYPE> R;
   const ExchangeCall& c = p.c;
   for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
     const int64_t token = item / p.segments;
     const int segment = (int)(item - token * p.segments);
-    const Piece<TYPE> piece(segment * kCopyThreads + threadIdx.x, c.cols);
+    const Piece<TYPE, ROWS> piece(segment * blockDim.x + threadIdx.x, c.cols);
+    const Slots slots(c, token);
     float sum[R::N] = {};
     for (int first = 0; first < c.top_k; first += kSlots) {
       u32x4 v[kSlots];
-      int row[kSlots];
 #pragma unroll
       for (int u = 0; u < kSlots; ++u) {
-        row[u] = slot_row(c, token, first + u);
-        if (row[u] >= 0) v[u] = piece.get(c.sorted, row[u], c.ldsorted, c.cols);
+        const int row = slots.row_of(first + u);
+        if (row >= 0) v[u] = piece.template get<true>(c.sorted, row, c.ldsorted, c.cols);
       }
 #pragma unroll
       for (int u = 0; u < kSlots; ++u) {
-        if (row[u] < 0) continue;
-        const float w = c.w != nullptr ? c.w[token * c.top_k + first + u] : 1.0f;
+        if (slots.row_of(first + u) < 0) continue;
+        const float w = slots.weight_of(first + u);
         float x[R::N];
         R::wide(v[u], x);
 #pragma unroll
@@ -339,51 +365,45 @@ __global__ void __launch_bounds__(kCopyThreads) combine_kernel(ExchangeArgs p) {
 }
 
 // One workgroup a token, since dw sums over its whole row.
-template <int TYPE>
+template <int TYPE, Rows ROWS>
 __global__ void __launch_bounds__(kCopyThreads) combine_grad_kernel(ExchangeArgs p) {
   typedef Row16<TYPE> R;
   const ExchangeCall& c = p.c;
   __shared__ float part[kCopyThreads / kWave][kSlots];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   for (int64_t token = blockIdx.x; token < c.tokens; token += gridDim.x) {
+    const Slots slots(c, token);
     for (int first = 0; first < c.top_k; first += kSlots) {
-      int row[kSlots];
-      float w[kSlots], dot[kSlots] = {};
-#pragma unroll
-      for (int u = 0; u < kSlots; ++u) {
-        row[u] = slot_row(c, token, first + u);
-        w[u] = row[u] >= 0 && c.w != nullptr ? c.w[token * c.top_k + first + u] : 1.0f;
-      }
+      float dot[kSlots] = {};
       for (int segment = 0; segment < p.segments; ++segment) {
-        const Piece<TYPE> piece(segment * kCopyThreads + threadIdx.x, c.cols);
-        const u32x4 dv = piece.get(c.tok, token, c.ldtok, c.cols);
+        const Piece<TYPE, ROWS> piece(segment * blockDim.x + threadIdx.x, c.cols);
         u32x4 v[kSlots];
         if (c.dw != nullptr) {
 #pragma unroll
-          for (int u = 0; u < kSlots; ++u)
-            if (row[u] >= 0) v[u] = piece.get(c.sorted, row[u], c.ldsorted, c.cols);
-        }
-        float dy[R::N];
-        R::wide(dv, dy);
-        if (c.out != nullptr) {
-#pragma unroll
           for (int u = 0; u < kSlots; ++u) {
-            if (row[u] < 0) continue;
-            float y[R::N];
-#pragma unroll
-            for (int e = 0; e < R::N; ++e) y[e] = w[u] * dy[e];
-            piece.put(c.out, row[u], c.ldout, c.cols, R::narrow(y));
+            const int row = slots.row_of(first + u);
+            if (row >= 0) v[u] = piece.template get<true>(c.sorted, row, c.ldsorted, c.cols);
           }
         }
-        if (c.dw != nullptr && piece.inside) {
+        float dy[R::N];
+        R::wide(piece.get(c.tok, token, c.ldtok, c.cols), dy);
 #pragma unroll
-          for (int u = 0; u < kSlots; ++u) {
-            if (row[u] < 0) continue;
+        for (int u = 0; u < kSlots; ++u) {
+          const int row = slots.row_of(first + u);
+          if (row < 0) continue;
+          if (c.out != nullptr) {
+            const float w = slots.weight_of(first + u);
+            float y[R::N];
+#pragma unroll
+            for (int e = 0; e < R::N; ++e) y[e] = w * dy[e];
+            piece.put(c.out, row, c.ldout, c.cols, R::narrow(y));
+          }
+          if (c.dw != nullptr && piece.inside) {
             float x[R::N];
             R::wide(v[u], x);
 #pragma unroll
             for (int e = 0; e < R::N; ++e)   // (a value of two pieces counts once)
-              if (e >= piece.fresh) dot[u] = __builtin_fmaf(dy[e], x[e], dot[u]);
+              if (e >= piece.shared) dot[u] = __builtin_fmaf(dy[e], x[e], dot[u]);
           }
         }
       }
@@ -400,7 +420,8 @@ __global__ void __launch_bounds__(kCopyThreads) combine_grad_kernel(ExchangeArgs
       if (u < kSlots && first + u < c.top_k) {
         float sum = 0.0f;
 #pragma unroll
-        for (int x = 0; x < kCopyThreads / kWave; ++x) sum += part[x][u];
+        for (int x = 0; x < kCopyThreads / kWave; ++x)
+          if (x < (int)blockDim.x / kWave) sum += part[x][u];
         c.dw[token * c.top_k + first + u] = sum;
       }
       __syncthreads();
@@ -410,37 +431,60 @@ __global__ void __launch_bounds__(kCopyThreads) combine_grad_kernel(ExchangeArgs
 
 namespace {
 
-ExchangeArgs exchange_args(const ExchangeCall& c) {
-  const int n = c.type == GEMM_TYPE_F32 ? 4 : 8;
-  const int pieces = (int)(((int64_t)c.cols + n - 1) / n);
-  const int segments = (pieces + kCopyThreads - 1) / kCopyThreads;
-  return ExchangeArgs{c, segments, (int64_t)c.tokens * segments};
-}
 unsigned grid_of(int64_t items) { return (unsigned)(items < (1 << 22) ? items : 1 << 22); }
 
 }  // namespace
 
-#define LASG_BY_TYPE(kernel, items)                                                              \
-  switch (c.type) {                                                                              \
-    case GEMM_TYPE_F32: kernel<GEMM_TYPE_F32><<<grid_of(items), kCopyThreads, 0, s>>>(p); break; \
-    case GEMM_TYPE_F16: kernel<GEMM_TYPE_F16><<<grid_of(items), kCopyThreads, 0, s>>>(p); break; \
-    default: kernel<GEMM_TYPE_BF16><<<grid_of(items), kCopyThreads, 0, s>>>(p); break;           \
-  }                                                                                              \
+// A piece a thread, as few workgroups a row as hold it: a row of 2050 values takes five waves, not
+// two workgroups of four (the second for one piece).
+#define LASG_LAUNCH(kernel, rows, items)                                                \
+  switch (c.type) {                                                                     \
+    case GEMM_TYPE_F32:                                                                 \
+      kernel<GEMM_TYPE_F32, rows><<<grid_of(items), threads, 0, s>>>(p);                \
+      break;                                                                            \
+    case GEMM_TYPE_F16:                                                                 \
+      kernel<GEMM_TYPE_F16, rows><<<grid_of(items), threads, 0, s>>>(p);                \
+      break;                                                                            \
+    default: kernel<GEMM_TYPE_BF16, rows><<<grid_of(items), threads, 0, s>>>(p);        \
+  }
+#define LASG_BY_TYPE(kernel, whole, items)                                              \
+  const int n = c.type == GEMM_TYPE_F32 ? 4 : 8;                                        \
+  const int pieces = (int)(((int64_t)c.cols + n - 1) / n);                              \
+  const int segments = (pieces + kCopyThreads - 1) / kCopyThreads;                      \
+  const int each = segments > 0 ? (pieces + segments - 1) / segments : 1;               \
+  const unsigned threads = (unsigned)(each + kWave - 1) / kWave * kWave;                \
+  const ExchangeArgs p{c, segments, (int64_t)c.tokens * segments};                      \
+  if (c.cols < n) {                                                                     \
+    LASG_LAUNCH(kernel, NARROW, items)                                                  \
+  } else if (whole) {                                                                   \
+    LASG_LAUNCH(kernel, WHOLE, items)                                                   \
+  } else {                                                                              \
+    LASG_LAUNCH(kernel, ANY, items)                                                     \
+  }                                                                                     \
   return hipGetLastError()
 
+namespace {
+
+// Whether every sorted row that is read is whole 128-byte lines.
+bool whole_lines(const ExchangeCall& c) {
+  const int64_t size = c.type == GEMM_TYPE_F32 ? 4 : 2;
+  return c.cols * size % 128 == 0 && c.ldsorted * size % 128 == 0 &&
+         reinterpret_cast<uintptr_t>(c.sorted) % 128 == 0;
+}
+
+}  // namespace
+
 hipError_t launch_dispatch(const ExchangeCall& c, hipStream_t s) {
-  const ExchangeArgs p = exchange_args(c);
-  LASG_BY_TYPE(dispatch_kernel, p.items);
+  LASG_BY_TYPE(dispatch_kernel, false, p.items);
 }
 hipError_t launch_combine(const ExchangeCall& c, hipStream_t s) {
-  const ExchangeArgs p = exchange_args(c);
-  LASG_BY_TYPE(combine_kernel, p.items);
+  LASG_BY_TYPE(combine_kernel, whole_lines(c), p.items);
 }
 hipError_t launch_combine_grad(const ExchangeCall& c, hipStream_t s) {
-  const ExchangeArgs p = exchange_args(c);
-  LASG_BY_TYPE(combine_grad_kernel, (int64_t)c.tokens);
+  LASG_BY_TYPE(combine_grad_kernel, whole_lines(c), (int64_t)c.tokens);
 }
 
 #undef LASG_BY_TYPE
+#undef LASG_LAUNCH
 
 }  // namespace lasg
