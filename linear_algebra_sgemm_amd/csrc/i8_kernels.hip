@@ -259,7 +259,7 @@ hipError_t launch_ksplit(const I8Call& c, hipStream_t s) {
 //    by 28672 x 4096 64 x 128 25, 64 x 64 28, 32 x 128 30.
 //  * K-split tiles of m x n take (m + n) K bytes through a CU's load path at 23 bytes a ns: 1 x
 //    4096 x 4096 16 x 16 6.4 us, 64 x 64 through LDS 10.6; off 16-byte boundaries about 2.5 times
-//    that (128 x 4096 x 4095: 64 x 32 52 us, 32 x 32 67, 128 x 128 through registers 88).
+//    that (64 x 4096 x 4095: 32 x 32 34 us, 128 x 128 through registers 49; 128 x 4096: 64 x 32 52, 48).
 int i8_tile(const I8Call& c, int cus, int force) {
   struct Tile {
     int m, n, per_cu;
@@ -268,7 +268,7 @@ int i8_tile(const I8Call& c, int cus, int force) {
   static const Tile kTiles[7] = {{256, 256, 1, 1250, 1840, 1840}, {128, 256, 2, 970, 1140, 1910},
                                  {128, 128, 2, 700, 760, 1130},   {64, 128, 2, 440, 470, 750},
                                  {64, 64, 2, 320, 330, 480},      {32, 128, 2, 350, 360, 540},
-                                 {128, 128, 2, 2600, 2600, 2700}};
+                                 {128, 128, 2, 1420, 1500, 1910}};
   static const int kSplit[5][2] = {{64, 32}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
   const int64_t b_rows = i8_b_rows(c);
   // 32-bit row, column and tile numbers in the tiled kernels.

@@ -251,6 +251,7 @@ i8_tile_kernel(I8TileArgs p) {
   u32x4 held[T::LOADS];
   auto load_tile = [&](int t) __attribute__((always_inline)) {
     const int k0 = block_of(t) * kBlockK;
+    const bool cut = T::DIRECT || k0 + kBlockK > c.K;
 #pragma unroll
     for (int v = 0; v < T::LOADS; ++v) {
       int row, chunk;
@@ -258,7 +259,7 @@ i8_tile_kernel(I8TileArgs p) {
       const int8_t* at = v < T::A_LOADS ? a_tile + a_row(row) * c.lda
                                         : b_tile + (int64_t)b_row(row) * c.ldb;
       const int k = k0 + 16 * chunk;
-      held[v] = k0 + kBlockK <= c.K ? load16(at + k) : load16_row(at, k, c.K);
+      held[v] = cut ? load16_row(at, k, c.K) : load16(at + k);
     }
   };
   auto store_tile = [&](int t) __attribute__((always_inline)) {
@@ -288,10 +289,11 @@ i8_tile_kernel(I8TileArgs p) {
   const uint32_t swizzled = 16 * (half ^ ((l32 >> 1) & 7));
   const uint32_t a_frag = (wm * T::WTM + l32) * kBlockK;
   const uint32_t b_frag = T::B_AT + (wn * T::WTN + l32) * kBlockK;
-  auto read_a = [&](I8Frags<T>& f, int t, int s) __attribute__((always_inline)) {
+  auto read_a = [&](I8Frags<T>& f, int t, int s, int blocks = T::FM) __attribute__((always_inline)) {
     const uint8_t* st = lds + t % T::STAGES * T::A_BYTES + (swizzled ^ (32 * s)) + a_frag;
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(st + i * 32 * kBlockK);
+    for (int i = 0; i < T::FM; ++i)
+      if (i < blocks) f.a[i] = *reinterpret_cast<const i32x4*>(st + i * 32 * kBlockK);
   };
   auto read_b = [&](I8Frags<T>& f, int t, int s) __attribute__((always_inline)) {
     const uint8_t* st = lds + (T::OWN_B ? 0 : t % T::STAGES * T::B_BYTES) + (swizzled ^ (32 * s)) + b_frag;
@@ -356,14 +358,17 @@ i8_tile_kernel(I8TileArgs p) {
 
   // The same for waves that own their rows of B: all of a K tile's fragments of B are
   // read at its start, then their one stage takes the next tile's; one meeting, at the
-  // start.
-  auto k_tile_own = [&](int t, auto copy_next) __attribute__((always_inline)) {
-    constexpr bool COPY = decltype(copy_next)::value;
+  // start.  PART: of the tile's rows of A only the first `live` blocks of 32 exist, as at the
+  // end of a group; the others are neither copied nor multiplied (1024 tokens, 128 rows a
+  // group on average, on 64 experts of 2048 x 4096 163 us without, 143 with).
+  const int live = m_end - m0 >= T::BM ? T::FM : (m_end - m0 + 31) / 32;
+  auto k_tile_own = [&](int t, auto copy_next, auto part) __attribute__((always_inline)) {
+    constexpr bool COPY = decltype(copy_next)::value, PART = decltype(part)::value;
     wait_vmcnt<0>();
     lds_barrier();
     I8Frags<T> b1, b2, b3;   // (their fragments of B only)
     read_b(f0, t, 0);
-    read_a(f0, t, 0);
+    read_a(f0, t, 0, PART ? live : T::FM);
     read_b(b1, t, 1);
     read_b(b2, t, 2);
     read_b(b3, t, 3);
@@ -373,27 +378,28 @@ i8_tile_kernel(I8TileArgs p) {
 #pragma unroll
       for (int x = 0; x < T::BLOCKS; ++x) {
         const int i = x / T::FN, j = x % T::FN;
-        sum[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b.b[j], a.a[i], sum[i][j], 0, 0, 0);
+        if (!PART || i < live)
+          sum[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b.b[j], a.a[i], sum[i][j], 0, 0, 0);
         if constexpr (COPY) {
 #pragma unroll
           for (int v = first + x * count / T::BLOCKS; v < first + (x + 1) * count / T::BLOCKS; ++v) {
             __builtin_amdgcn_sched_barrier(0);
-            copy(t + 1, v);
+            if (!PART || v >= T::A_LOADS || (wave * T::A_LOADS + v) * 8 < 32 * live) copy(t + 1, v);
             __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    read_a(f1, t, 1);
+    read_a(f1, t, 1, PART ? live : T::FM);
     step(f0, f0, 0, T::A_LOADS);
     if constexpr (COPY) {
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(0xC07F);   // this wave's fragments of B are read
     }
-    read_a(f0, t, 2);
+    read_a(f0, t, 2, PART ? live : T::FM);
     step(f1, b1, T::A_LOADS, T::B_LOADS / 2);
-    read_a(f1, t, 3);
+    read_a(f1, t, 3, PART ? live : T::FM);
     step(f0, b2, T::A_LOADS + T::B_LOADS / 2, T::B_LOADS - T::B_LOADS / 2);
     step(f1, b3, 0, 0);
   };
@@ -408,8 +414,13 @@ i8_tile_kernel(I8TileArgs p) {
         for (int v = 0; v < T::LOADS; ++v) copy(0, v);
       }
       int t = 0;
-      for (; t + 1 < kts; ++t) k_tile_own(t, std::true_type());
-      k_tile_own(t, std::false_type());
+      if (!T::GROUPED || live == T::FM) {
+        for (; t + 1 < kts; ++t) k_tile_own(t, std::true_type(), std::false_type());
+        k_tile_own(t, std::false_type(), std::false_type());
+      } else if constexpr (T::GROUPED) {
+        for (; t + 1 < kts; ++t) k_tile_own(t, std::true_type(), std::true_type());
+        k_tile_own(t, std::false_type(), std::true_type());
+      }
     }
   } else if (kts > 0) {
     if constexpr (T::DIRECT) {
@@ -510,7 +521,9 @@ hipError_t launch_i8_tile(const I8Call& c, int tile, hipStream_t s) {
     case 3: return launch_tile<64, 128, 2, 2, 3, true, false>(c, s);
     case 4: return launch_tile<64, 64, 2, 2, 4, true, false>(c, s);
     case 5: return launch_tile<32, 128, 1, 4, 4, true, false>(c, s);
-    default: return launch_tile<128, 128, 2, 2, 2, false, false>(c, s);
+    // (Eight waves, since each holds what it loads: 4096 x 4096 x 4095 127 us, with four 184, with
+    // sixteen 163; 64 x 14336 x 4095 49, 79 and 43.)
+    default: return launch_tile<128, 128, 2, 4, 2, false, false>(c, s);
   }
 }
 
