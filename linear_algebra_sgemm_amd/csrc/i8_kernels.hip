@@ -89,156 +89,165 @@ __global__ void __launch_bounds__(512) i8_ksplit_kernel(I8Call p) {
   const int r = lane % 16, g = lane / 16;
   const int64_t b_rows = i8_b_rows(p);
   const unsigned tiles_n = (unsigned)((b_rows + 16 * NF - 1) / (16 * NF));
-  int64_t total;
-  GroupTiles<16 * MF> tiles(p);
-  if constexpr (GROUPED)
-    total = (int64_t)tiles.total * tiles_n;
-  else
-    total = (((int64_t)p.M + 16 * MF - 1) / (16 * MF)) * tiles_n;
+  const GroupTiles<16 * MF> tiles(p);
+  const unsigned tiles_m = GROUPED ? (unsigned)tiles.total : ((unsigned)p.M + 16 * MF - 1) / (16 * MF);
   const int full = p.K / kBlockK;
-  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
-    const unsigned tm = (unsigned)(t / tiles_n), tn = (unsigned)(t - (int64_t)tm * tiles_n);
-    int group = 0, m0 = (int)(tm * 16 * MF), m_end = p.M;
-    if constexpr (GROUPED) {
-      tiles.find(p, (int)tm, group, m0, m_end);
-      if (m0 >= m_end) continue;
-    }
-    const int8_t* b_mat = p.B + group * b_rows * p.ldb;
-    const float* sb_v = p.SB + group * b_rows;
-    const float* bias_v = p.bias == nullptr ? nullptr : p.bias + group * b_rows;
-    // The row of B behind row x of fragment j (past the end: the last; not stored).
-    const auto b_row = [&](int j, int x) -> int64_t {
-      const int64_t f = (int64_t)tn * NF + j;
-      if (!p.gated) {
-        const int64_t row = 16 * f + x;
-        return row < p.N ? row : p.N - 1;
+  for (unsigned tm = blockIdx.y; tm < tiles_m; tm += gridDim.y)
+    for (unsigned tn = blockIdx.x; tn < tiles_n; tn += gridDim.x) {
+      int group = 0, m0 = (int)(tm * 16 * MF), m_end = p.M;
+      if constexpr (GROUPED) {
+        tiles.find(p, (int)tm, group, m0, m_end);
+        if (m0 >= m_end) continue;
       }
-      const int64_t row = 8 * f + x % 8;
-      return (row < p.N ? row : p.N - 1) + (x >= 8 ? p.N : 0);
-    };
-    const int8_t* ap[MF];
-    const int8_t* bp[NF];
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      const int row = m0 + 16 * i + r < m_end ? m0 + 16 * i + r : m_end - 1;
-      ap[i] = p.A + i8_a_row(p, row) * p.lda;
-    }
-#pragma unroll
-    for (int j = 0; j < NF; ++j) bp[j] = b_mat + b_row(j, r) * p.ldb;
-    i32x4 sums[MF * NF];
-#pragma unroll
-    for (int f = 0; f < MF * NF; ++f) sums[f] = i32x4{0, 0, 0, 0};
-    // (B first: the lane then holds four columns of one row of C)
-    const auto multiply = [&](const Frag8 (&a)[MF], const Frag8 (&b)[NF])
-        __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) sums[i * NF + j] = add_product(b[j], a[i], sums[i * NF + j]);
-    };
-    const auto load_a = [&](Frag8 (&a)[MF], int k0) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < MF; ++i) load_frag(a[i], ap[i], lane, k0);
-    };
-    const auto load_b = [&](Frag8 (&b)[NF], int k0) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < NF; ++j) load_frag(b[j], bp[j], lane, k0);
-    };
-    const int first = (int)((int64_t)full * wave / 8), end = (int)((int64_t)full * (wave + 1) / 8);
-    if constexpr (GROUP > 1) {
-      for (int kb = first; kb < end; kb += GROUP) {
-        Frag8 a[GROUP][MF], b[GROUP][NF];
-#pragma unroll
-        for (int u = 0; u < GROUP; ++u) {
-          const int at = kb + u < end ? kb + u : end - 1;   // (an extra read, not used)
-          load_b(b[u], at * kBlockK);
-          load_a(a[u], at * kBlockK);
+      const int8_t* b_mat = p.B + group * b_rows * p.ldb;
+      const float* sb_v = p.SB + group * b_rows;
+      const float* bias_v = p.bias == nullptr ? nullptr : p.bias + group * b_rows;
+      // The row of B behind row x of fragment j (past the end: the last; not stored).
+      const auto b_row = [&](int j, int x) -> int64_t {
+        const int64_t f = (int64_t)tn * NF + j;
+        if (!p.gated) {
+          const int64_t row = 16 * f + x;
+          return row < p.N ? row : p.N - 1;
         }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < GROUP; ++u)
-          if (kb + u < end) multiply(a[u], b[u]);
-      }
-    } else if (first < end) {
-      Frag8 b[2][NF];
-      load_b(b[0], first * kBlockK);
-      // Two blocks a turn, so that the buffers of B keep their registers.
-      for (int kb = first; kb < end; kb += 2) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (kb + u >= end) break;
-          Frag8 a[MF];
-          load_a(a, (kb + u) * kBlockK);
-          load_b(b[1 - u], (kb + u + 1 < end ? kb + u + 1 : kb + u) * kBlockK);
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(a, b[u]);
-        }
-      }
-    }
-    if (full * kBlockK < p.K && wave == 7) {   // the last, shorter block
-#pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        Frag8 b;
-        load_frag_tail(b, bp[j], lane, full * kBlockK, p.K);
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          Frag8 a;
-          load_frag_tail(a, ap[i], lane, full * kBlockK, p.K);
-          sums[i * NF + j] = add_product(b, a, sums[i * NF + j]);
-        }
-      }
-    }
-    // Waves 4 to 7 put their sums down, waves 0 to 3 add theirs (half the space).
-    if (wave >= 4) {
-#pragma unroll
-      for (int f = 0; f < MF * NF; ++f) part[wave - 4][f][lane] = sums[f];
-    }
-    __syncthreads();
-    if (wave < 4) {
-#pragma unroll
-      for (int f = 0; f < MF * NF; ++f) part[wave][f][lane] += sums[f];
-    }
-    __syncthreads();
-    for (int f = wave; f < MF * NF; f += 8) {
-      const int i = f / NF, j = f % NF;
-      const int row = m0 + 16 * i + r;
-      const bool live = row < m_end && (!p.gated || g < 2);
-      if (!live) continue;
-      const SplitScale sa(p.K == 0 ? 0.0f : p.SA[i8_a_row(p, row)]);
-      // This lane's four columns of B (with a gate their counterparts are 32 lanes on).
-      const auto value = [&](int l, f32x4& u) __attribute__((always_inline)) {
-        const i32x4 v = (part[0][f][l] + part[1][f][l]) + (part[2][f][l] + part[3][f][l]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t n = b_row(j, 4 * (l / 16) + e);
-          const SplitScale sb(p.K == 0 ? 0.0f : sb_v[n]);
-          u[e] = i8_scaled(v[e], sa.m, sa.e, sb.m, sb.e, p.alpha, bias_v != nullptr ? bias_v[n] : 0.0f);
-        }
+        const int64_t row = 8 * f + x % 8;
+        return (row < p.N ? row : p.N - 1) + (x >= 8 ? p.N : 0);
       };
-      f32x4 v;
-      value(lane, v);
+      const int8_t* ap[MF];
+      const int8_t* bp[NF];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = apply_act(v[e], p.act);
-      int64_t col = ((int64_t)tn * NF + j) * 16 + 4 * g;
-      if (p.gated) {
-        f32x4 u;
-        value(lane + 32, u);
-        v *= u;
-        col = ((int64_t)tn * NF + j) * 8 + 4 * g;
+      for (int i = 0; i < MF; ++i) {
+        const int row = m0 + 16 * i + r < m_end ? m0 + 16 * i + r : m_end - 1;
+        ap[i] = p.A + i8_a_row(p, row) * p.lda;
       }
-      if (col < p.N) store_c(p, row, col, v);
+#pragma unroll
+      for (int j = 0; j < NF; ++j) bp[j] = b_mat + b_row(j, r) * p.ldb;
+      // What this wave needs at the end: it finishes fragment `wave`, a lane four columns of one row
+      // (with a gate the lanes of the first half, whose counterparts are 32 lanes on).
+      static_assert(MF * NF <= 8, "a fragment a wave");
+      const int end_row = m0 + 16 * (wave / NF) + r, end_j = wave % NF;
+      const bool ends = wave < MF * NF && end_row < m_end && (!p.gated || g < 2);
+      float sa = 0.0f, sb[2][4] = {}, bias[2][4] = {};
+      if (ends) {
+        if (p.K != 0) sa = p.SA[i8_a_row(p, end_row)];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (h == 1 && !p.gated) continue;
+            const int64_t n = b_row(end_j, 4 * g + 8 * h + e);
+            if (p.K != 0) sb[h][e] = sb_v[n];
+            if (bias_v != nullptr) bias[h][e] = bias_v[n];
+          }
+      }
+      i32x4 sums[MF * NF];
+#pragma unroll
+      for (int f = 0; f < MF * NF; ++f) sums[f] = i32x4{0, 0, 0, 0};
+      // (B first: the lane then holds four columns of one row of C)
+      const auto multiply = [&](const Frag8 (&a)[MF], const Frag8 (&b)[NF])
+          __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+          for (int j = 0; j < NF; ++j) sums[i * NF + j] = add_product(b[j], a[i], sums[i * NF + j]);
+      };
+      const auto load_a = [&](Frag8 (&a)[MF], int k0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) load_frag(a[i], ap[i], lane, k0);
+      };
+      const auto load_b = [&](Frag8 (&b)[NF], int k0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) load_frag(b[j], bp[j], lane, k0);
+      };
+      const int first = (int)((int64_t)full * wave / 8), end = (int)((int64_t)full * (wave + 1) / 8);
+      if constexpr (GROUP > 1) {
+        for (int kb = first; kb < end; kb += GROUP) {
+          Frag8 a[GROUP][MF], b[GROUP][NF];
+#pragma unroll
+          for (int u = 0; u < GROUP; ++u) {
+            const int at = kb + u < end ? kb + u : end - 1;   // (an extra read, not used)
+            load_b(b[u], at * kBlockK);
+            load_a(a[u], at * kBlockK);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int u = 0; u < GROUP; ++u)
+            if (kb + u < end) multiply(a[u], b[u]);
+        }
+      } else if (first < end) {
+        Frag8 b[2][NF];
+        load_b(b[0], first * kBlockK);
+        // Two blocks a turn, so that the buffers of B keep their registers.
+        for (int kb = first; kb < end; kb += 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (kb + u >= end) break;
+            Frag8 a[MF];
+            load_a(a, (kb + u) * kBlockK);
+            load_b(b[1 - u], (kb + u + 1 < end ? kb + u + 1 : kb + u) * kBlockK);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(a, b[u]);
+          }
+        }
+      }
+      if (full * kBlockK < p.K && wave == 7) {   // the last, shorter block
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          Frag8 b;
+          load_frag_tail(b, bp[j], lane, full * kBlockK, p.K);
+#pragma unroll
+          for (int i = 0; i < MF; ++i) {
+            Frag8 a;
+            load_frag_tail(a, ap[i], lane, full * kBlockK, p.K);
+            sums[i * NF + j] = add_product(b, a, sums[i * NF + j]);
+          }
+        }
+      }
+      // Waves 4 to 7 put their sums down, waves 0 to 3 add theirs (half the space).
+      if (wave >= 4) {
+#pragma unroll
+        for (int f = 0; f < MF * NF; ++f) part[wave - 4][f][lane] = sums[f];
+      }
+      __syncthreads();
+      if (wave < 4) {
+#pragma unroll
+        for (int f = 0; f < MF * NF; ++f) part[wave][f][lane] += sums[f];
+      }
+      __syncthreads();
+      if (ends) {
+        const SplitScale ma(sa);
+        const auto value = [&](int h) __attribute__((always_inline)) {
+          const int l = lane + 32 * h;
+          const i32x4 v = (part[0][wave][l] + part[1][wave][l]) + (part[2][wave][l] + part[3][wave][l]);
+          f32x4 u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const SplitScale mb(sb[h][e]);
+            u[e] = i8_scaled(v[e], ma.m, ma.e, mb.m, mb.e, p.alpha, bias[h][e]);
+          }
+          return u;
+        };
+        f32x4 v = value(0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = apply_act(v[e], p.act);
+        int64_t col = ((int64_t)tn * NF + end_j) * 16 + 4 * g;
+        if (p.gated) {
+          const f32x4 u = value(1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] *= u[e];
+          col = ((int64_t)tn * NF + end_j) * 8 + 4 * g;
+        }
+        if (col < p.N) store_c(p, end_row, col, v);
+      }
+      __syncthreads();   // the next tile reuses the LDS array
     }
-    __syncthreads();   // the next tile reuses the LDS array
-  }
 }
 
 namespace {
 
 template <int MF, int NF>
 hipError_t launch_ksplit(const I8Call& c, hipStream_t s) {
-  const int64_t tn = (i8_b_rows(c) + 16 * NF - 1) / (16 * NF);
-  const int64_t total = i8_tiles_m(c, 16 * MF) * tn;
-  const unsigned grid = (unsigned)(total < (1 << 22) ? total : 1 << 22);
+  const int64_t tn = (i8_b_rows(c) + 16 * NF - 1) / (16 * NF), tm = i8_tiles_m(c, 16 * MF);
+  const dim3 grid((unsigned)(tn < (1 << 20) ? tn : 1 << 20), (unsigned)(tm < 32768 ? tm : 32768));
   if (c.groups > 0)
     i8_ksplit_kernel<MF, NF, true><<<grid, 512, 0, s>>>(c);
   else
