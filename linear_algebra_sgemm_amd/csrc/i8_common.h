@@ -72,7 +72,9 @@ struct GroupTiles {
       const int y = __shfl_up(sum, d);
       if (lane >= d) sum += y;
     }
-    total = __builtin_amdgcn_readlane(sum, kWave - 1);
+    // (Offsets that do not ascend may add up to more than the call was launched for, or past 2^31.)
+    const int all = __builtin_amdgcn_readlane(sum, kWave - 1), most = (int)i8_tiles_m(c, BM);
+    total = all < 0 ? 0 : all < most ? all : most;
   }
   // 0 <= t < total.  Of offsets that do not ascend a tile may come out empty (row >=
   // end), but never outside 0 .. M.

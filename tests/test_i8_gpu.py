@@ -374,6 +374,33 @@ def test_matrices_past_4_gib(tile):
         assert torch.equal(c[:, -40:].cpu(), want)
 
 
+@pytest.mark.parametrize("tile", [-1, 0, 1, 2, 3, 4, 5, 8])
+def test_offsets_between_2_and_4_gib(tile):
+    """Rows of A read by index, and the second half of a gated B, begin past 2^31 bytes of the first."""
+    N, K, rows = 140000, 16384, 3 * 2 ** 30 // 16384
+    g = torch.Generator().manual_seed(2)
+    a = torch.zeros((rows, K), dtype=torch.int8, device="cuda")
+    tail = int8s(g, 2, K)
+    a[-2:] = tail.cuda()
+    b = torch.zeros((2 * N, K), dtype=torch.int8, device="cuda")
+    last = int8s(g, 2, 40, K)
+    b[N - 40:N], b[2 * N - 40:] = last[0].cuda(), last[1].cuda()
+    sa, sb = torch.ones(rows, device="cuda"), torch.full((2 * N,), 2.0 ** -10, device="cuda")
+    index = torch.tensor([rows - 1, rows - 2], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    c = torch.zeros((2, N), device="cuda")
+    note("i8 grouped between 2 and 4 GiB tile %d" % tile)
+    lib.gemm_debug_force_i8_tile(tile)
+    lib.i8_gemm_grouped(1, offsets, 2, N, K, 1.0, a, K, sa, rows, index, 1, b, K, sb, None, 0, True,
+                        lib.TYPE_F32, c, N)
+    torch.cuda.synchronize()
+    lib.gemm_debug_force_i8_tile(-1)
+    x, one = tail[[1, 0]], torch.ones(2)
+    y, bound = reference_product(x, one, last.view(80, K), torch.full((80,), 2.0 ** -10), 1.0, None, 0, True,
+                                 torch.float32)
+    assert ((c[:, -40:].cpu().double() - y).abs() <= bound).all() and not c[:, :-40].any()
+
+
 def test_random_shapes():
     g = torch.Generator().manual_seed(11)
     for i in range(30):
