@@ -10,9 +10,9 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // The tiled kernels (i8_tile_kernels.hip): tiles 0 to 6 of i8_tile.  Tiles 0 to 5
-// copy straight into LDS, which the call has to allow (i8_direct).
+// copy straight into LDS, which the call has to allow (i8_direct); `once`: B past the caches.
 bool i8_direct(const I8Call& c);
-hipError_t launch_i8_tile(const I8Call& c, int tile, hipStream_t s);
+hipError_t launch_i8_tile(const I8Call& c, int tile, bool once, hipStream_t s);
 
 // Rows of B, of a group where there are groups.
 __host__ __device__ __forceinline__ int64_t i8_b_rows(const I8Call& c) {

@@ -257,27 +257,51 @@ hipError_t launch_ksplit(const I8Call& c, hipStream_t s) {
 
 }  // namespace
 
+namespace {
+
+// Groups that have rows, and rows of such a group, as if rows were spread at random.
+struct Spread {
+  double active, each;
+  explicit Spread(const I8Call& c) {
+    const double rows = c.M, groups = c.groups > 0 ? c.groups : 1;
+    active = c.groups > 0 ? groups * (1 - __builtin_exp(-rows / groups)) : 1;
+    each = rows / active;
+  }
+};
+
+struct Tile {
+  int m, n, per_cu;
+  double one, every, all;   // see the rule
+};
+const Tile kTiles[7] = {{256, 256, 1, 1250, 1840, 1840}, {128, 256, 2, 970, 1140, 1910},
+                        {128, 128, 2, 700, 760, 1130},   {64, 128, 2, 440, 470, 750},
+                        {64, 64, 2, 320, 330, 480},      {32, 128, 2, 350, 360, 540},
+                        {128, 128, 2, 1420, 1500, 1910}};
+
+// Whether tiles of `m` rows read B once, more of it than stays in the 256 MB last-level cache from
+// one call to the next with others between: then it is copied past the caches.  4 tokens on 64 experts of
+// 2048 x 4096 (218 MB) 41 us without, 37 with; 16 tokens 83 and 74, 512 102 and 89; 64 rows by 28672 x
+// 4096 (117 MB) 25.2 and 22.6.  A weight of 59 MB that is used again at once takes 12 us, and 15.
+bool reads_once(const I8Call& c, int m) {
+  const Spread x(c);
+  return x.active * (double)i8_b_rows(c) * c.K >= 96e6 && x.each <= (c.groups > 0 ? 0.7 : 1.0) * m;
+}
+
+}  // namespace
+
 // The rule takes the tile of the least estimated time.  Measured on 256 CUs:
 //  * tiles through LDS take a time per block of K that depends on how many of them
 //    run, not on the shape: kTiles has it in ns for one of them, for one on every CU and for as
 //    many as fit a CU.  4096 x 4096 x 4096: 256 x 256 62 us, 128 x 256 65, 128 x 128 73; 4096 x 14336 x
 //    4096, 3.5 rounds of either: 241 and 228; 1024 x 4096 x 4096: 128 x 128 26, 128 x 256 33; 1024
 //    x 1024 x 4096: 64 x 64 11.1, 64 x 128 14.8, 128 x 128 23.9.
-//  * where the weights bound a call it takes their bytes at 5.5 TB/s, and the bytes that the
-//    CUs load at 40: 4 tokens on 64 experts of 2048 x 4096 32 x 128 tiles 41 us, 64 x 64 45; 64 rows
-//    by 28672 x 4096 64 x 128 25, 64 x 64 28, 32 x 128 30.
+//  * where the weights bound a call it takes their bytes at 5.5 TB/s (6.3 past the caches), and the
+//    bytes that the CUs load at 40: 4 tokens on 64 experts of 2048 x 4096 32 x 128 tiles 37 us, 64
+//    x 64 40; 64 rows by 28672 x 4096 64 x 128 22.6, 64 x 64 25, 32 x 128 29.
 //  * K-split tiles of m x n take (m + n) K bytes through a CU's load path at 23 bytes a ns: 1 x
 //    4096 x 4096 16 x 16 6.4 us, 64 x 64 through LDS 10.6; off 16-byte boundaries about 2.5 times
 //    that (64 x 4096 x 4095: 32 x 32 34 us, 128 x 128 through registers 49; 128 x 4096: 64 x 32 52, 48).
 int i8_tile(const I8Call& c, int cus, int force) {
-  struct Tile {
-    int m, n, per_cu;
-    double one, every, all;
-  };
-  static const Tile kTiles[7] = {{256, 256, 1, 1250, 1840, 1840}, {128, 256, 2, 970, 1140, 1910},
-                                 {128, 128, 2, 700, 760, 1130},   {64, 128, 2, 440, 470, 750},
-                                 {64, 64, 2, 320, 330, 480},      {32, 128, 2, 350, 360, 540},
-                                 {128, 128, 2, 1420, 1500, 1910}};
   static const int kSplit[5][2] = {{64, 32}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
   const int64_t b_rows = i8_b_rows(c);
   // 32-bit row, column and tile numbers in the tiled kernels.
@@ -286,15 +310,14 @@ int i8_tile(const I8Call& c, int cus, int force) {
   const bool direct = i8_direct(c);
   int tile = force;
   if (tile < 0) {
-    // Groups with rows, and rows of such a group, as if they were spread at random.
-    const double rows = c.M, groups = c.groups > 0 ? c.groups : 1;
-    const double active = c.groups > 0 ? groups * (1 - __builtin_exp(-rows / groups)) : 1;
-    const double each = rows / active;
+    const Spread x(c);
     const auto tiles = [&](int m, int n) {
-      const double down = c.groups == 0 ? __builtin_ceil(rows / m) : each <= 0.7 * m ? 1 : each / m + 0.5;
-      return active * down * (double)((b_rows + n - 1) / n);
+      const double down = c.groups == 0      ? __builtin_ceil((double)c.M / m)
+                          : x.each <= 0.7 * m ? 1
+                                              : x.each / m + 0.5;
+      return x.active * down * (double)((b_rows + n - 1) / n);
     };
-    const double weights = active * (double)b_rows * c.K;
+    const double weights = x.active * (double)b_rows * c.K;
     double best = 1e30;
     const auto offer = [&](int t, double cost) {
       if (cost < best) {
@@ -303,16 +326,16 @@ int i8_tile(const I8Call& c, int cus, int force) {
       }
     };
     for (int t = direct ? 0 : 6; tiled && t < (direct ? 6 : 7); ++t) {
-      const Tile& x = kTiles[t];
-      const double n = tiles(x.m, x.n), round = (double)x.per_cu * cus;
+      const Tile& k = kTiles[t];
+      const double n = tiles(k.m, k.n), round = (double)k.per_cu * cus;
       const double full = __builtin_floor(n / round), left = n - full * round, on = left / cus;
-      double last = on <= 1 ? x.one + on * (x.every - x.one) : x.every + (on - 1) * (x.all - x.every);
+      double last = on <= 1 ? k.one + on * (k.every - k.one) : k.every + (on - 1) * (k.all - k.every);
       if (left == 0) last = 0;
       // (after whole rounds a CU's only workgroup gains little from the others' absence)
-      else if (full > 0 && x.per_cu == 1 && last < 0.85 * x.all) last = 0.85 * x.all;
+      else if (full > 0 && k.per_cu == 1 && last < 0.85 * k.all) last = 0.85 * k.all;
       const double blocks = (double)((c.K + kBlockK - 1) / kBlockK) + 2;   // (2: start and end)
-      const double work = blocks * (full * x.all + last);
-      const double bytes = weights / 5500 + n * (x.m + x.n) * c.K / 40000;
+      const double work = blocks * (full * k.all + last);
+      const double bytes = weights / (reads_once(c, k.m) ? 6300 : 5500) + n * (k.m + k.n) * c.K / 40000;
       offer(t, work > bytes ? work : bytes);
     }
     for (int i = 0; i < 5; ++i) {
@@ -334,7 +357,7 @@ hipError_t launch_i8_gemm(const I8Call& c, int cus, int force, hipStream_t s) {
     case 9: return launch_ksplit<2, 1>(c, s);
     case 10: return launch_ksplit<1, 2>(c, s);
     case 11: return launch_ksplit<1, 1>(c, s);
-    default: return launch_i8_tile(c, tile, s);
+    default: return launch_i8_tile(c, tile, reads_once(c, kTiles[tile].m), s);
   }
 }
 

@@ -22,11 +22,12 @@
 namespace lasg {
 
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, bool DIRECT_, bool OWN_B_,
-          bool GROUPED_>
+          bool GROUPED_, bool ONCE_>
 struct I8Tile {
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr int STAGES = STAGES_;
   static constexpr bool DIRECT = DIRECT_, GROUPED = GROUPED_;
+  static constexpr bool ONCE = ONCE_;   // B is copied past the caches
   static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = WAVES * kWave;
   static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
   static constexpr int FM = WTM / 32, FN = WTN / 32, BLOCKS = FM * FN;
@@ -244,8 +245,11 @@ i8_tile_kernel(I8TileArgs p) {
     }
   }
   auto copy = [&](int t, int v) __attribute__((always_inline)) {
-    dma16_sbase_u((v < T::A_LOADS ? a_tile : b_tile) + block_of(t) * kBlockK, off[v],
-                  lds_base + slot_at(v, t));
+    const int8_t* base = (v < T::A_LOADS ? a_tile : b_tile) + block_of(t) * kBlockK;
+    if (T::ONCE && v >= T::A_LOADS)
+      dma16_sbase_once(base, off[v], lds_base + slot_at(v, t));
+    else
+      dma16_sbase_u(base, off[v], lds_base + slot_at(v, t));
   };
   // K tile t through registers, any alignment: loaded, and later stored.
   u32x4 held[T::LOADS];
@@ -481,7 +485,7 @@ i8_tile_kernel(I8TileArgs p) {
 namespace {
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool DIRECT, bool OWN_B>
-hipError_t launch_tile(const I8Call& c, hipStream_t s) {
+hipError_t launch_tile(const I8Call& c, bool once, hipStream_t s) {
   const int tiles_m = (int)i8_tiles_m(c, BM);
   const int tiles_n = (int)((i8_b_rows(c) + BN - 1) / BN);
   // Where the bytes of the weights bound the call (groups; few rows) different weights start at different K,
@@ -490,14 +494,16 @@ hipError_t launch_tile(const I8Call& c, hipStream_t s) {
   // slower with it, since tiles side by side then read A at different times.
   const I8TileArgs p{c, tiles_m, tiles_n, c.groups > 0 ? 4 : 8, c.groups > 0 ? 11 : 0,
                      c.groups == 0 && c.M <= 256 ? 11 : 0};
-  const dim3 grid((unsigned)tiles_m * tiles_n);
-  if (c.groups > 0) {
-    typedef I8Tile<BM, BN, WM, WN, STAGES, DIRECT, OWN_B, true> T;
-    i8_tile_kernel<T><<<grid, T::THREADS, 0, s>>>(p);
-  } else {
-    typedef I8Tile<BM, BN, WM, WN, STAGES, DIRECT, OWN_B, false> T;
-    i8_tile_kernel<T><<<grid, T::THREADS, 0, s>>>(p);
-  }
+  const dim3 grid((unsigned)tiles_m * tiles_n), block(WM * WN * kWave);
+  once = once && DIRECT;
+  if (c.groups > 0 && once)
+    i8_tile_kernel<I8Tile<BM, BN, WM, WN, STAGES, DIRECT, OWN_B, true, DIRECT>><<<grid, block, 0, s>>>(p);
+  else if (c.groups > 0)
+    i8_tile_kernel<I8Tile<BM, BN, WM, WN, STAGES, DIRECT, OWN_B, true, false>><<<grid, block, 0, s>>>(p);
+  else if (once)
+    i8_tile_kernel<I8Tile<BM, BN, WM, WN, STAGES, DIRECT, OWN_B, false, DIRECT>><<<grid, block, 0, s>>>(p);
+  else
+    i8_tile_kernel<I8Tile<BM, BN, WM, WN, STAGES, DIRECT, OWN_B, false, false>><<<grid, block, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -513,17 +519,17 @@ bool i8_direct(const I8Call& c) {
          b_rows * c.ldb < (1ll << 32);
 }
 
-hipError_t launch_i8_tile(const I8Call& c, int tile, hipStream_t s) {
+hipError_t launch_i8_tile(const I8Call& c, int tile, bool once, hipStream_t s) {
   switch (tile) {
-    case 0: return launch_tile<256, 256, 2, 4, 2, true, false>(c, s);
-    case 1: return launch_tile<128, 256, 1, 4, 2, true, true>(c, s);
-    case 2: return launch_tile<128, 128, 2, 2, 2, true, false>(c, s);
-    case 3: return launch_tile<64, 128, 2, 2, 3, true, false>(c, s);
-    case 4: return launch_tile<64, 64, 2, 2, 4, true, false>(c, s);
-    case 5: return launch_tile<32, 128, 1, 4, 4, true, false>(c, s);
+    case 0: return launch_tile<256, 256, 2, 4, 2, true, false>(c, once, s);
+    case 1: return launch_tile<128, 256, 1, 4, 2, true, true>(c, once, s);
+    case 2: return launch_tile<128, 128, 2, 2, 2, true, false>(c, once, s);
+    case 3: return launch_tile<64, 128, 2, 2, 3, true, false>(c, once, s);
+    case 4: return launch_tile<64, 64, 2, 2, 4, true, false>(c, once, s);
+    case 5: return launch_tile<32, 128, 1, 4, 4, true, false>(c, once, s);
     // (Eight waves, since each holds what it loads: 4096 x 4096 x 4095 127 us, with four 184, with
     // sixteen 163; 64 x 14336 x 4095 49, 79 and 43.)
-    default: return launch_tile<128, 128, 2, 4, 2, false, false>(c, s);
+    default: return launch_tile<128, 128, 2, 4, 2, false, false>(c, once, s);
   }
 }
 

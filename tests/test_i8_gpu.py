@@ -401,6 +401,18 @@ def test_offsets_between_2_and_4_gib(tile):
     assert ((c[:, -40:].cpu().double() - y).abs() <= bound).all() and not c[:, :-40].any()
 
 
+@pytest.mark.parametrize("rows", [None, [5, 0, 27, 1]])
+def test_weights_larger_than_the_caches(rows):
+    """About 100 MB of weights for few rows: copied past the caches."""
+    M, N = (31, 6001) if rows is None else (40, 1501)
+    p = Product(M, N, 8208, pad=1, gated=True, act=2, type_="f32", rows=rows, first=0)
+    assert p.b.numel() >= 96e6
+    for tile in range(-1, 6):
+        note("i8 product of 100 MB of weights, tile %d, rows %s" % (tile, rows))
+        p.c.fill_(77.0)
+        run(p, tile)
+
+
 def test_random_shapes():
     g = torch.Generator().manual_seed(11)
     for i in range(30):
