@@ -213,7 +213,8 @@ typedef struct {
 int moe_ffn_workspace(const moe_shape_t* shape, size_t* bytes);
 
 /*
- * The layer, for the few tokens of a decoding step:
+ * The layer, for the few tokens of a decoding step (more go through moe_sort and
+ * i8_gemm_grouped):
  *   l = X R^T (T x E),  ids[t] = the k largest of l[t], largest first, equal
  *   ones by lower number,  w[t] = softmax(l[t]) at ids[t] (divided by their sum
  *   with norm_topk),  Y[t] = sum_s w[t][s] W2[e] h(W1[e] X[t]),  e = ids[t][s],
