@@ -20,8 +20,9 @@
 // cycles, where a library's int8 product reaches 2075 to 2170 TOP/s; the waves' fragment
 // reads and the copies fill LDS's 128 bytes a cycle meanwhile.  4096 x 14336 x 4096 with bias and
 // GELU 237 to 249 us.  For few rows the weights' bytes: 4 tokens on 64 experts of 2048 x
-// 4096 37 us (6.0 TB/s), 64 x 28672 x 4096 22.5 (5.3 TB/s).  Between them the small tiles' chain of
-// meeting, read and four dependent MFMAs, 0.32 us a K tile: 256 x 4096 x 4096 11.6 us.
+// 4096 37 us (6.0 TB/s), 64 x 28672 x 4096 22.5 (5.3 TB/s).  Between them the copies into
+// LDS, which reach 25 to 32 bytes a cycle and CU in all tiles (64 x 64: 16 KB in 0.32 us), with
+// more of them on their way no more: 256 x 4096 x 4096 11.6 us.
 #include <type_traits>
 
 #include "dma_common.h"
