@@ -72,6 +72,15 @@ struct I8TileArgs {
 
 namespace {
 
+// dma16_sbase_u for lines that nobody else will read: they are not kept in the caches.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // m0 is listed as clobbered on purpose
+__device__ __forceinline__ void dma16_sbase_once(const void* base, uint32_t offset, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds_base)), "v"(offset), "s"(base) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 template <class T>
 struct I8Frags {
   i32x4 a[T::FM], b[T::FN];
