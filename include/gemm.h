@@ -331,7 +331,7 @@ int moe_combine(int tokens, int top_k, int cols, int type, const void* X, int ld
  * dw FP32 (tokens x top_k dense), 0 for entries outside 0 .. x_rows - 1; dX x_rows x cols (lddx), of
  * which rows that no entry names are left as they were, and no two may name the same.  Either dX
  * or dw may be NULL: then it is not wanted (without dw X is not read).  dX must not
- * overlap X or dY.
+ * overlap X or dY.  x_rows == 0 or cols == 0: dw is all zeros, and dY, X and dX are not touched.
  */
 int moe_combine_grad(int tokens, int top_k, int cols, int type, const void* dY, int lddy,
                      const void* X, int ldx, int x_rows, const int* pos, const float* w,

@@ -265,10 +265,11 @@ int moe_combine_grad(int tokens, int top_k, int cols, int type, const void* dY, 
   const bool rows = tokens > 0 && cols > 0 && x_rows > 0;
   if (rows && (dY == nullptr || (dw != nullptr && X == nullptr))) return GEMM_STATUS_INVALID_VALUE;
   if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
-  // (Without columns dw is all zeros still.)
-  if (tokens == 0 || (cols == 0 && dw == nullptr)) return GEMM_STATUS_SUCCESS;
-  const lasg::ExchangeCall c{tokens, top_k, cols, type, dY, lddy, X, ldx, rows ? x_rows : 0, pos, w,
-                             dX, lddx, dw};
+  // Without columns or sorted rows there is no dX, dw is all zeros, and dY and X, which may be null
+  // then, are not read: the kernel sees a call without columns.
+  if (tokens == 0 || (!rows && dw == nullptr)) return GEMM_STATUS_SUCCESS;
+  const lasg::ExchangeCall c{tokens, top_k, rows ? cols : 0, type, dY, lddy, X, ldx,
+                             rows ? x_rows : 0, pos, w, dX, lddx, dw};
   return finish(lasg::launch_combine_grad(c, stream));
 }
 
