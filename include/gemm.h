@@ -260,8 +260,9 @@ int i8_quantize(int rows, int cols, int type, const void* X, int ldx,
  * every row of B, `act` of gemm_act_t, C (ldc >= N) of `type` F32, F16 or BF16, rounded
  * once to nearest even.  K is at most 131071: the sums are exact, in int32, and are
  * rounded to fp32 once before they are scaled.  All values of int8 may occur, -128
- * too.  Bytes of A and B past column K are not used.  alpha == 0 or K == 0: A, B and the
- * scales are not read.  With a gate N is at most 2^30.
+ * too.  Bytes of A and B past column K are not used.  alpha, the scales and the sum are
+ * multiplied without a detour past fp32's range: only their product has to be inside it.  alpha == 0 or
+ * K == 0: A, B and the scales are not read.  With a gate N is at most 2^30.
  */
 int i8_gemm_bias_act(int M, int N, int K, float alpha,
                      const int8_t* A, int lda, const float* SA,

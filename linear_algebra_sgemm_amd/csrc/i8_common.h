@@ -26,15 +26,16 @@ __host__ __device__ __forceinline__ int64_t i8_tiles_m(const I8Call& c, int bm) 
   return most > whole ? most : whole;
 }
 
-// A scale as mantissa and exponent, so that the product of a sum and its two
-// scales neither underflows nor overflows before it is whole.
+// A scale as mantissa and exponent, so that the product of a sum, its two scales and
+// alpha (I8Call) neither underflows nor overflows before it is whole: the exponents of all three are
+// added first (alpha's to the row's), and alpha's mantissa, at least 1, comes last, in one fma with the bias.
 struct SplitScale {
   float m;
   int e;
-  __device__ __forceinline__ explicit SplitScale(float s)
-      : m(__builtin_amdgcn_frexp_mantf(s)), e(__builtin_amdgcn_frexp_expf(s)) {}
+  __device__ __forceinline__ explicit SplitScale(float s, int more = 0)
+      : m(__builtin_amdgcn_frexp_mantf(s)), e(__builtin_amdgcn_frexp_expf(s) + more) {}
 };
-// alpha sa sb sum + bias: the sum is exact and is rounded to fp32 here, once.
+// alpha sa sb sum + bias (ea with alpha's exponent): the sum is exact and is rounded to fp32 here, once.
 __device__ __forceinline__ float i8_scaled(int sum, float ma, int ea, float mb, int eb, float alpha,
                                            float bias) {
   return __builtin_fmaf(alpha, __builtin_ldexpf((float)sum * (ma * mb), ea + eb), bias);

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(512) i8_ksplit_kernel(I8Call p) {
       }
       __syncthreads();
       if (ends) {
-        const SplitScale ma(sa);
+        const SplitScale ma(sa, p.alpha_e);
         const auto value = [&](int h) __attribute__((always_inline)) {
           const int l = lane + 32 * h;
           const i32x4 v = (part[0][wave][l] + part[1][wave][l]) + (part[2][wave][l] + part[3][wave][l]);

@@ -486,7 +486,7 @@ i8_tile_kernel(I8TileArgs p) {
       mb[2 * T::BN + x] = bias;
     }
     if (x < T::BM) {
-      const SplitScale s(sa);
+      const SplitScale s(sa, c.alpha_e);
       ma[x] = s.m;
       reinterpret_cast<int*>(ma)[T::BM + x] = s.e;
     }

@@ -3,6 +3,7 @@
 // quick returns, and the launch.  None of these calls allocates, copies to the host or uses the library's own
 // workspace, so all may be captured into a graph and run on any stream.
 #include <atomic>
+#include <cmath>
 
 #include "../../include/gemm_debug.h"
 #include "lm_launch.h"
@@ -167,8 +168,14 @@ int i8_product(bool grouped, int groups, const int* offsets, int M, int N, int K
     return GEMM_STATUS_INVALID_VALUE;
   if (!lasg::library_ready()) return GEMM_STATUS_NOT_INITIALIZED;
   if (empty) return GEMM_STATUS_SUCCESS;
-  const lasg::I8Call c{M, N, reads_ab ? K : 0, alpha, A, lda, SA, reads_ab ? index : nullptr, a_rows,
-                       per, B, ldb, SB, bias, act, gated, type, C, ldc, groups, offsets};
+  int alpha_e = 0;
+  if (std::isfinite(alpha) && alpha != 0.0f) {
+    alpha = 2.0f * std::frexp(alpha, &alpha_e);
+    --alpha_e;
+  }
+  const lasg::I8Call c{M, N, reads_ab ? K : 0, alpha, A, lda, SA, reads_ab ? index : nullptr,
+                       a_rows, per, B, ldb, alpha_e, SB, bias, act, gated, type, C, ldc, groups,
+                       offsets};
   return finish(lasg::launch_i8_gemm(c, lasg::library_cus(), g_force_i8_tile.load(), stream));
 }
 
