@@ -48,6 +48,12 @@ __device__ __forceinline__ void group_rows(const I8Call& c, int g, int& begin, i
   end = e < begin ? begin : e < c.M ? e : c.M;
 }
 
+// Tiles of BM rows that `rows` >= 0 take.  (Unsigned: of up to 2^31 - 1 rows the sum passes int.)
+template <int BM>
+__device__ __forceinline__ int tiles_of(int rows) {
+  return (int)(((unsigned)rows + BM - 1) / BM);
+}
+
 // The tiles of BM rows of all groups, in order: their number, and tile t's
 // group and rows.  A wave works it out alone: lane l looks after the groups l, ...
 // of `per` consecutive ones, whose tiles are summed over the lanes.
@@ -64,7 +70,7 @@ struct GroupTiles {
       if (g < c.groups) {
         int b, e;
         group_rows(c, g, b, e);
-        mine += (e - b + BM - 1) / BM;
+        mine += tiles_of<BM>(e - b);
       }
     }
     sum = mine;
@@ -87,11 +93,11 @@ struct GroupTiles {
     const int last = group + per < c.groups ? group + per - 1 : c.groups - 1;
     int b, e;
     group_rows(c, group, b, e);
-    while (left >= (e - b + BM - 1) / BM && group < last) {
-      left -= (e - b + BM - 1) / BM;
+    while (left >= tiles_of<BM>(e - b) && group < last) {
+      left -= tiles_of<BM>(e - b);
       group_rows(c, ++group, b, e);
     }
-    const bool good = left >= 0 && left < (e - b + BM - 1) / BM;
+    const bool good = left >= 0 && left < tiles_of<BM>(e - b);
     group = __builtin_amdgcn_readfirstlane(group);
     row = __builtin_amdgcn_readfirstlane(good ? b + left * BM : e);
     end = __builtin_amdgcn_readfirstlane(e);

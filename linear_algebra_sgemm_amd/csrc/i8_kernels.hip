@@ -112,11 +112,13 @@ __global__ void __launch_bounds__(512) i8_ksplit_kernel(I8Call p) {
         const int64_t row = 8 * f + x % 8;
         return (row < p.N ? row : p.N - 1) + (x >= 8 ? p.N : 0);
       };
+      // (Rows are compared from m0 on: m0 plus the tile's height may pass 2^31.)
+      const int rows = m_end - m0;
       const int8_t* ap[MF];
       const int8_t* bp[NF];
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        const int row = m0 + 16 * i + r < m_end ? m0 + 16 * i + r : m_end - 1;
+        const int row = 16 * i + r < rows ? m0 + 16 * i + r : m_end - 1;
         ap[i] = p.A + i8_a_row(p, row) * p.lda;
       }
 #pragma unroll
@@ -124,8 +126,9 @@ __global__ void __launch_bounds__(512) i8_ksplit_kernel(I8Call p) {
       // What this wave needs at the end: it finishes fragment `wave`, a lane four columns of one row
       // (with a gate the lanes of the first half, whose counterparts are 32 lanes on).
       static_assert(MF * NF <= 8, "a fragment a wave");
-      const int end_row = m0 + 16 * (wave / NF) + r, end_j = wave % NF;
-      const bool ends = wave < MF * NF && end_row < m_end && (!p.gated || g < 2);
+      const int end_at = 16 * (wave / NF) + r, end_j = wave % NF;
+      const int end_row = m0 + (end_at < rows ? end_at : 0);
+      const bool ends = wave < MF * NF && end_at < rows && (!p.gated || g < 2);
       float sa = 0.0f, sb[2][4] = {}, bias[2][4] = {};
       if (ends) {
         if (p.K != 0) sa = p.SA[i8_a_row(p, end_row)];
