@@ -213,8 +213,8 @@ typedef struct {
 int moe_ffn_workspace(const moe_shape_t* shape, size_t* bytes);
 
 /*
- * The layer, for the few tokens of a decoding step (more go through moe_sort and
- * i8_gemm_grouped):
+ * The layer, for the few tokens of a decoding step.  (More tokens, with int8 weights and with
+ * experts and weights of the caller's own router: moe_sort, i8_gemm_grouped, moe_combine.)
  *   l = X R^T (T x E),  ids[t] = the k largest of l[t], largest first, equal
  *   ones by lower number,  w[t] = softmax(l[t]) at ids[t] (divided by their sum
  *   with norm_topk),  Y[t] = sum_s w[t][s] W2[e] h(W1[e] X[t]),  e = ids[t][s],
@@ -263,6 +263,8 @@ int i8_quantize(int rows, int cols, int type, const void* X, int ldx,
  * too.  Bytes of A and B past column K are not used.  alpha, the scales and the sum are
  * multiplied without a detour past fp32's range: only their product has to be inside it.  alpha == 0 or
  * K == 0: A, B and the scales are not read.  With a gate N is at most 2^30.
+ * (Where M times the rows of B pass about 2^34, or either passes 2^30, a result takes some seven
+ * times as long.)
  */
 int i8_gemm_bias_act(int M, int N, int K, float alpha,
                      const int8_t* A, int lda, const float* SA,

@@ -281,10 +281,18 @@ const Tile kTiles[7] = {{256, 256, 1, 1250, 1840, 1840}, {128, 256, 2, 970, 1140
                         {64, 64, 2, 320, 330, 480},      {32, 128, 2, 350, 360, 540},
                         {128, 128, 2, 1420, 1500, 1910}};
 
-// Whether tiles of `m` rows read B once, more of it than stays in the 256 MB last-level cache from
-// one call to the next with others between: then it is copied past the caches.  4 tokens on 64 experts of
-// 2048 x 4096 (218 MB) 41 us without, 37 with; 16 tokens 83 and 74, 512 102 and 89; 64 rows by 28672 x
-// 4096 (117 MB) 25.2 and 22.6.  A weight of 59 MB that is used again at once takes 12 us, and 15.
+// Whether tiles of `m` rows read B once, and at least 96 MB of it: then it is copied past the caches.
+// That is better where other weights are used before this one comes again, as in a model of many layers, and
+// worse where the next call uses it too, which up to about 250 MB finds it in the last-level cache.  In
+// us, without and with, other weights between | the same at once (64 x 128 and 32 x 128 tiles):
+//   64 rows by 20480 x 4096 (84 MB)   24.5, 21.6 | 15.4, 20.3      36864 (151 MB)  41.8, 37.7 | 29.8, 36.1
+//   by 28672 x 4096 (117 MB)          28.1, 23.7 | 19.7, 22.3      61440 (252 MB)  51.2, 43.4 | 36.9, 41.8
+//   4 tokens on 64 experts (25 used): of 1024 x 4096 (111 MB)      23.2, 20.6 | 17.8, 17.8
+//                                     of 2048 x 4096 (222 MB)      40.5, 36.3 | 30.5, 32.9
+// A call does not say what comes between.  That weights of 96 MB and more have others between them,
+// and smaller ones may not, is a guess: those would gain as well (61 MB 22.6, 20.5) and lose more (14.7, 19.1).
+// Groups count as read once while nearly all fit one tile: rows spread at random vary by the root of
+// their mean, so that at a mean of 0.7 x 32 two deviations more are 32.
 bool reads_once(const I8Call& c, int m) {
   const Spread x(c);
   return x.active * (double)i8_b_rows(c) * c.K >= 96e6 && x.each <= (c.groups > 0 ? 0.7 : 1.0) * m;
@@ -307,7 +315,8 @@ bool reads_once(const I8Call& c, int m) {
 int i8_tile(const I8Call& c, int cus, int force) {
   static const int kSplit[5][2] = {{64, 32}, {32, 32}, {32, 16}, {16, 32}, {16, 16}};
   const int64_t b_rows = i8_b_rows(c);
-  // 32-bit row, column and tile numbers in the tiled kernels.
+  // 32-bit row, column and tile numbers in the tiled kernels, and fewer than 2^32 threads a launch.  (A
+  // larger call takes K-split tiles: 131328 x 131072 x 4096 472 ms, 130816 x 131072 x 4096 66.5.)
   const bool tiled = c.M <= (1 << 30) && b_rows <= (1 << 30) &&
                      i8_tiles_m(c, 32) * ((b_rows + 63) / 64) < (1 << 23);
   const bool direct = i8_direct(c);

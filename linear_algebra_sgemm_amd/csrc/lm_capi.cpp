@@ -1,7 +1,7 @@
 // C ABI of the 8-bit operators, the mixture-of-experts layer and the exchange of
 // tokens with the experts' order (declared in include/gemm.h): argument checks,
-// quick returns, and the launch.  None of these calls allocates, copies to the host or uses the library's own
-// workspace, so all may be captured into a graph and run on any stream.
+// quick returns, and the launch.  None of these calls allocates, copies to the host or
+// uses the library's own workspace, so all may be captured into a graph and run on any stream.
 #include <atomic>
 #include <cmath>
 
