@@ -323,6 +323,7 @@ int i8_tile(const I8Call& c, int cus, int force) {
   int tile = force;
   if (tile < 0) {
     const Spread x(c);
+    // (Groups of 0.7 m rows take one tile, as in reads_once; of longer ones the last is half full.)
     const auto tiles = [&](int m, int n) {
       const double down = c.groups == 0      ? __builtin_ceil((double)c.M / m)
                           : x.each <= 0.7 * m ? 1
